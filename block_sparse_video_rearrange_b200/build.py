@@ -11,7 +11,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "librf.so")
-SOURCES = ["rf_plan.cu", "rf_rearrange.cu", "rf_select.cu", "rf_attn.cu", "rf_noalloc.cu", "rf_selftest.cu"]
+SOURCES = ["rf_plan.cu", "rf_rearrange.cu", "rf_select.cu", "rf_attn.cu", "rf_noalloc.cu", "rf_selftest.cu",
+           "rf_diff.cu", "rf_diff_attn.cu", "rf_diff_bwd.cu", "rf_norm.cu"]
 
 
 def nvcc_path():

@@ -1,0 +1,1007 @@
+// Backward pass of differential attention over the selected key blocks.
+//
+// With P_w = softmax(scale Q_w K_w^T) (w = 1, 2), A = P_1 - lambda P_2 and
+// O = A V per query head, and dO given:
+//   dV  = A^T dO                      dA = dO V^T
+//   dS_1 = P_1 o (dA - delta_1)       dS_2 = -lambda P_2 o (dA - delta_2)
+//   dQ_w = scale dS_w K_w             dK_w = scale dS_w^T Q_w
+//   delta_w = rowsum(P_w o dA) = dO . O_w,  dlambda = -sum of delta_2 over rows
+// (o: element by element).  P_w is recomputed from S_w and the log2-sum the
+// forward pass kept.  delta_w is taken from the fp32 O_w the forward pass kept:
+// where a softmax is nearly one-hot, dA - delta cancels almost completely, and
+// a 16-bit O_w in its place gave dQ errors of 2e-2 on such rows (fp32: 4e-3, as
+// with an exact delta).
+//
+// Kernels:
+//   rf_diff_prep_bwd_kernel  per (query block, head): delta_1, delta_2 and the
+//                            kept sums packed per row; the block's part of
+//                            dlambda; one bit per listed key block, by key block.
+//   rf_diff_dq_kernel        CTA = (query block, head): dQ over the listed blocks.
+//   rf_diff_dkv_kernel       CTA = (key block, key/value head): dK and dV over
+//                            every (head of the group, query block) that lists
+//                            it, in ascending order.
+//   rf_diff_dlam_kernel      sums dlambda's parts in block order.
+// Two passes (S and dA computed in both, 7 matrix products for 5) need no
+// atomic additions, so the gradients are the same bits every time.
+//
+// A and dS are rounded once, to the inputs' type, for the tensor cores.  fp16
+// has no room for their range, so there A and dS carry a power of two chosen
+// from the tensors' largest |dO|, |V| and |lambda| (exact to undo): the bound
+// on |dS| lands at 2^15, values down to 2^-29 of it stay normal.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "rf_device.cuh"
+#include "rf_tiles.cuh"
+
+namespace {
+
+constexpr int kThreads = 640;      // four compute warpgroups and one of single-warp roles
+constexpr int kCompute = 512;
+constexpr int kMmaWarp = 16;       // TMEM allocation and every tcgen05.mma
+constexpr int kLoadWarp = 17;      // dQ: Q, dO, K; dK/dV: everything
+constexpr int kLoadVWarp = 18;     // dQ: V
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kBoxBytes = RF_BLOCK * 128;
+constexpr uint32_t kHalf = 64 * 128;  // bytes of 64 rows of a box
+constexpr uint32_t kStatBytes = 4 * RF_BLOCK * 4;
+
+struct BwdArgs {
+  RfGeomDev g;
+  const int32_t* sel_idx;
+  const int32_t* sel_num;
+  const float* lambda;       // [n1]
+  const float* stats;        // [n1][t_qblk][4][128]: -lse_1, -lse_2, delta_1, delta_2
+  const uint32_t* bits;      // [n1][t_qblk][words]
+  const uint32_t* amax;      // fp16: largest |dO|, |V|, |lambda| as fp32 bits
+  int words;
+  uint16_t* dq;
+  uint16_t* dk;
+  uint16_t* dv;
+  uint32_t* status;
+  float scale;
+  float sl2;                 // scale * log2(e)
+};
+
+// Power-of-two exponents that A and dS carry through the 16-bit rounding.
+template <int D, bool kBf16>
+__device__ __forceinline__ void carry_exponents(const uint32_t* amax, int& ea, int& es) {
+  ea = es = 0;
+  if constexpr (!kBf16) {
+    const float mdo = __uint_as_float(amax[0]), mv = __uint_as_float(amax[1]);
+    const float ml = fmaxf(1.f, __uint_as_float(amax[2]));
+    // |A| <= 1 + |lambda|, |dA|, |delta| <= D max|dO| max|V|
+    ea = max(14 - rf_ceil_log2(ml), -100);
+    const float bound = 2.0f * D * mdo * mv * ml;
+    if (bound > 0.f && bound < INFINITY) es = min(max(15 - rf_ceil_log2(bound), -100), 100);
+  }
+}
+
+template <int D>
+struct __align__(1024) DqSmem {
+  static constexpr int kTileBytes = RF_BLOCK * D * 2;
+  uint8_t q[kTileBytes];
+  uint8_t d_o[kTileBytes];
+  uint8_t k[2][kTileBytes];
+  uint8_t v[2][kTileBytes];
+  uint64_t bar_q, bar_aux;
+  uint64_t bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2];
+  uint64_t bar_sd_full[2];  // S_1, S_2 and dA of a 64-key half computed
+  uint64_t bar_ds_full[2];  // dS_1 and dS_2 of it stored (and all of S, dA read)
+  uint64_t bar_dq_done[2];  // dQ += dS K of it complete
+  uint64_t bar_final, bar_drain;
+  uint32_t tmem_base;
+  int abort;
+  int n_valid;
+  int list[RF_MAX_KV_LIST];
+};
+
+template <int D>
+struct __align__(1024) DkvSmem {
+  static constexpr int kTileBytes = RF_BLOCK * D * 2;
+  uint8_t k[kTileBytes];
+  uint8_t v[kTileBytes];
+  uint8_t q[2][kTileBytes];
+  uint8_t d_o[2][kTileBytes];
+  float stats[2][4][RF_BLOCK];
+  float lam[2];
+  uint64_t bar_kv, bar_aux;
+  uint64_t bar_full[2], bar_empty[2];
+  uint64_t bar_s1_full[2];  // by parity: S_1 of the next step is computed one step ahead
+  uint64_t bar_s2_full, bar_da_full;
+  uint64_t bar_ew;          // A, dS_1, dS_2 of a step stored
+  uint64_t bar_x_done;      // A and dS_1 read by their products
+  uint64_t bar_y_done;      // dS_2 too
+  uint64_t bar_final, bar_drain;
+  uint32_t tmem_base;
+  int abort;
+  int n_items;
+};
+
+// Zeroes rows [nrows, 128) of a tile's 128-byte-wide boxes (a row is 128 bytes
+// of each box whatever the swizzle), by one warp.
+__device__ __forceinline__ void zero_tail(uint8_t* tile, int boxes, int nrows, int lane) {
+  const int per_box = (RF_BLOCK - nrows) * 8;
+  for (int x = 0; x < boxes; ++x)
+    for (int i = lane; i < per_box; i += 32)
+      *reinterpret_cast<uint4*>(tile + x * kBoxBytes + nrows * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// dS of 32 keys of one map for one query row: P = 2^(s * sl2 + nlse), then
+// P * (dA * c - dc), rounded to 16 bits and packed.
+template <bool kBf16, bool kFull>
+__device__ __forceinline__ void ds_chunk(const uint32_t* s, const uint32_t* da, int c0, int vr, float sl2,
+                                         float nlse, float c, float dc, uint32_t* pk) {
+  const uint64_t sl = rf_f2(__float_as_uint(sl2), __float_as_uint(sl2));
+  const uint64_t nl = rf_f2(__float_as_uint(nlse), __float_as_uint(nlse));
+  const uint64_t cc = rf_f2(__float_as_uint(c), __float_as_uint(c));
+  const uint64_t nd = rf_f2(__float_as_uint(-dc), __float_as_uint(-dc));
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float x0, x1, y0, y1;
+    rf_f2_split(rf_fma2(rf_f2(s[i], s[i + 1]), sl, nl), x0, x1);
+    const uint64_t p = rf_f2(__float_as_uint(rf_ex2(x0)), __float_as_uint(rf_ex2(x1)));
+    rf_f2_split(rf_mul2(p, rf_fma2(rf_f2(da[i], da[i + 1]), cc, nd)), y0, y1);
+    if (!kFull) {
+      y0 = c0 + i < vr ? y0 : 0.f;
+      y1 = c0 + i + 1 < vr ? y1 : 0.f;
+    }
+    pk[i >> 1] = rf_pack2<kBf16>(y0, y1);
+  }
+}
+
+// N consecutive accumulator columns of this thread's row, times f, to 16 bits.
+template <int N, bool kBf16>
+__device__ __forceinline__ void store_row(uint32_t taddr, bool have, float f, bool live, uint16_t* dst) {
+  uint32_t o[N];
+  if (have) {
+    if constexpr (N == 32) tmem_ld32(taddr, o);
+    else                   tmem_ld16(taddr, o);
+    tmem_wait_ld();
+  }
+  if (!live) return;
+#pragma unroll
+  for (int c = 0; c < N / 8; ++c) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = have ? rf_pack2<kBf16>(f * __uint_as_float(o[8 * c + 2 * i]), f * __uint_as_float(o[8 * c + 2 * i + 1]))
+                  : 0u;
+    reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// dQ.  A step is (key block, 64-key half); the two halves use two sets of TMEM
+// columns (S_1, S_2, dA: 64 each at [192 h, +192)), so one half's matrix
+// products run while the other half's dS is computed.  Warpgroup e computes map
+// e % 2 of half e / 2 (thread = query row = TMEM lane) and writes dS over the
+// first half of that map's S columns.  dQ accumulates at [384, 512): 64 columns
+// per map (at D = 64 both maps' columns of the product, half of them unused, so
+// that every operand starts at a box).
+// Issue order after dS of step t: dQ(t), dA(t + 2), then - once dQ(t) has read
+// the dS columns, by which time dA runs - S_1 and S_2 of t + 2.
+// Bound: per 128 x 128 block the ex2 unit 2,048 cycles; the tensor pipe about
+// 2,100 (N = 64 products are fed from shared memory at two thirds of its rate).
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    rf_diff_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                      const __grid_constant__ BwdArgs a) {
+  using Smem = DqSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  constexpr int kBoxes = D * 2 / 128;
+  constexpr uint32_t kTileBytes = Smem::kTileBytes;
+  constexpr uint32_t kDq = 384;
+
+  const RfGeomDev& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = blockIdx.x / g.t_qblk, tb = blockIdx.x % g.t_qblk;
+  const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
+  const int nblk = s.n_pb + s.nb;
+  const int gk = n / (g.n1 / g.n2);
+  int q_r0, q_rows;
+  rf_block_span(s, tb - s.qblk_off, q_r0, q_rows);
+  volatile int* abort = &sm.abort;
+  const bool bnsd = g.layout == RF_LAYOUT_BNSD;
+  auto coords = [&](int heads, int head, int r0, int& c1, int& c2) {
+    if (bnsd) { c1 = r0; c2 = s.batch_idx * heads + head; }
+    else      { c1 = head; c2 = (int)s.row_off + r0; }
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(rf_smem_u32(&sm.bar_q), 1);
+    mbar_init(rf_smem_u32(&sm.bar_aux), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(rf_smem_u32(&sm.bar_k_full[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_k_empty[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_v_full[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_v_empty[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_sd_full[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_ds_full[i]), 256);
+      mbar_init(rf_smem_u32(&sm.bar_dq_done[i]), 1);
+    }
+    mbar_init(rf_smem_u32(&sm.bar_final), 1);
+    mbar_init(rf_smem_u32(&sm.bar_drain), 1);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(rf_smem_u32(&sm.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  const size_t row_id = (size_t)tb * g.n1 + n;
+  const int32_t* row = a.sel_idx + row_id * g.max_kv;
+  const int num_raw = a.sel_num[row_id];
+  const int num = num_raw < 0 ? 0 : (num_raw > g.max_kv ? g.max_kv : num_raw);
+  for (int c = threadIdx.x; c < num; c += kThreads) sm.list[c] = row[c];
+  __syncthreads();
+  if (warp == 0) {
+    int bad = 0;  // counted by the forward pass and the preparation
+    const int cnt = compact_ascending(sm.list, num, nblk, lane, &bad);
+    if (lane == 0) {
+      const bool stopped = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT) != 0;
+      sm.n_valid = stopped ? 0 : cnt;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  const int nv = sm.n_valid;
+  const int vr_last = s.Lp - (s.n_pb - 1) * RF_BLOCK;  // valid rows of the last prefix block
+  int ea, es;
+  carry_exponents<D, kBf16>(a.amax, ea, es);
+
+  if (warp >= 16) {
+    if ((warp == kLoadWarp || warp == kLoadVWarp) && nv > 0) {
+      // ---------------- TMA producers (lane 0 loads; the warp zeroes a partial block's tail) ----------------
+      const bool is_k = warp == kLoadWarp;
+      uint64_t* full = is_k ? sm.bar_k_full : sm.bar_v_full;
+      uint64_t* empty = is_k ? sm.bar_k_empty : sm.bar_v_empty;
+      uint8_t* tiles = is_k ? &sm.k[0][0] : &sm.v[0][0];
+      const void* map = is_k ? static_cast<const void*>(&tm_k) : static_cast<const void*>(&tm_v);
+      int c1, c2;
+      if (is_k && lane == 0) {
+        coords(g.n1, n, q_r0, c1, c2);
+        mbar_arrive_expect_tx(rf_smem_u32(&sm.bar_q), 2 * kTileBytes);
+        for (int x = 0; x < kBoxes; ++x) {
+          tma_load_3d(rf_smem_u32(sm.q + x * kBoxBytes), &tm_q, rf_smem_u32(&sm.bar_q), x * 64, c1, c2);
+          tma_load_3d(rf_smem_u32(sm.d_o + x * kBoxBytes), &tm_do, rf_smem_u32(&sm.bar_q), x * 64, c1, c2);
+        }
+      }
+      volatile int no_abort = 0;
+      int issued = 0, aux_used = 0;
+      for (int b = 0; b < nv; ++b) {
+        const int st = b & 1;
+        if (b >= 2 && !warp_wait(rf_smem_u32(&empty[st]), ((b >> 1) & 1) ^ 1, abort)) {
+          if (lane == 0) record_timeout(abort, a.status, is_k ? 4 : 5);
+          break;
+        }
+        const int blk = sm.list[b];
+        // K rows past the prefix meet dS = 0 in dQ: they must be finite.
+        const bool tail = is_k && blk == s.n_pb - 1 && vr_last < RF_BLOCK;
+        const uint32_t bar = rf_smem_u32(tail ? &sm.bar_aux : &full[st]);
+        if (lane == 0) {
+          int r0, nr;
+          rf_block_span(s, blk, r0, nr);
+          coords(g.n2, gk, r0, c1, c2);
+          mbar_arrive_expect_tx(bar, kTileBytes);
+          for (int x = 0; x < kBoxes; ++x)
+            tma_load_3d(rf_smem_u32(tiles + st * kTileBytes + x * kBoxBytes), map, bar, x * 64, c1, c2);
+        }
+        __syncwarp();
+        if (tail) {  // at most one block of a list
+          aux_used = 1;
+          const bool landed = warp_wait(bar, 0, &no_abort);
+          if (landed) zero_tail(tiles + st * kTileBytes, kBoxes, vr_last, lane);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (!landed) record_timeout(abort, a.status, 4);
+            mbar_arrive(rf_smem_u32(&full[st]));
+          }
+          __syncwarp();
+        }
+        issued = b + 1;
+      }
+      if (*abort) {
+        // Let this warp's own copies land before the shared memory goes away.
+        if (is_k) warp_wait(rf_smem_u32(&sm.bar_q), 0, &no_abort);
+        for (int b = (issued > 2 ? issued - 2 : 0); b < issued; ++b)
+          warp_wait(rf_smem_u32(&full[b & 1]), (b >> 1) & 1, &no_abort);
+        (void)aux_used;
+      }
+    } else if (warp == kMmaWarp && nv > 0) {
+      // ---------------- tcgen05.mma issue ----------------
+      const uint32_t fmt = kBf16 ? 1u : 0u;
+      const uint32_t id_sd = umma_idesc_f16(fmt, 128, 64, 0);
+      const uint32_t id_dq = umma_idesc_f16(fmt, 128, 64, 1);
+      const uint64_t dq = umma_desc_sw128(rf_smem_u32(sm.q), 16, 1024);
+      const uint64_t ddo = umma_desc_sw128(rf_smem_u32(sm.d_o), 16, 1024);
+      const uint64_t dk0 = umma_desc_sw128(rf_smem_u32(sm.k[0]), 16, 1024);
+      const uint64_t dv0 = umma_desc_sw128(rf_smem_u32(sm.v[0]), 16, 1024);
+      const uint64_t dkn0 = umma_desc_sw128(rf_smem_u32(sm.k[0]), kBoxBytes, 1024);
+      const int nt = 2 * nv;
+      auto issue_da = [&](int t) {  // dA of step t
+        const int b = t >> 1, h = t & 1;
+        const uint64_t dv = dv0 + (uint64_t)(((b & 1) * kTileBytes + h * kHalf) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + 192 * h + 128, ddo + off, dv + off, id_sd, kk > 0 ? 1u : 0u);
+        }
+        if (h == 1) tc_commit(rf_smem_u32(&sm.bar_v_empty[b & 1]));
+      };
+      auto issue_s = [&](int t) {  // S_1 and S_2 of step t
+        const int b = t >> 1, h = t & 1;
+        const uint64_t dk = dk0 + (uint64_t)(((b & 1) * kTileBytes + h * kHalf) >> 4);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) {
+            const int byte = w * D + kk * 32;
+            const uint32_t off = ((uint32_t)(byte >> 7) * kBoxBytes + (byte & 127)) >> 4;
+            mma_ss(tmem + 192 * h + 64 * w, dq + off, dk + off, id_sd, kk > 0 ? 1u : 0u);
+          }
+        tc_commit(rf_smem_u32(&sm.bar_sd_full[h]));
+      };
+      bool ok = warp_wait<true>(rf_smem_u32(&sm.bar_q), 0, abort) &&
+                warp_wait<true>(rf_smem_u32(&sm.bar_v_full[0]), 0, abort) &&
+                warp_wait<true>(rf_smem_u32(&sm.bar_k_full[0]), 0, abort);
+      if (ok) {
+        tc_fence_after();
+        if (elect_one()) {
+          issue_da(0);
+          issue_s(0);
+          issue_da(1);
+          issue_s(1);
+        }
+        __syncwarp();
+      }
+      for (int t = 0; ok && t < nt; ++t) {
+        const int b = t >> 1, h = t & 1, st = b & 1;
+        const uint32_t ph = b & 1;  // each half's barriers complete once per block
+        if (!warp_wait<true>(rf_smem_u32(&sm.bar_ds_full[h]), ph, abort)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t dk = dkn0 + (uint64_t)((st * kTileBytes + h * kHalf) >> 4);
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(tmem + kDq + 64 * w, tmem + 192 * h + 64 * w + 8 * kk,
+                     dk + (uint64_t)(((D == 128 ? w : 0) * kBoxBytes + kk * 2048) >> 4), id_dq,
+                     (t > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(rf_smem_u32(&sm.bar_dq_done[h]));
+          if (h == 1) tc_commit(rf_smem_u32(&sm.bar_k_empty[st]));
+        }
+        __syncwarp();
+        if (t + 2 < nt) {
+          const int b2 = b + 1;
+          const uint32_t ph2 = (b2 >> 1) & 1;
+          if (h == 0 && !warp_wait<true>(rf_smem_u32(&sm.bar_v_full[b2 & 1]), ph2, abort)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) issue_da(t + 2);
+          __syncwarp();
+          if (h == 0 && !warp_wait<true>(rf_smem_u32(&sm.bar_k_full[b2 & 1]), ph2, abort)) { ok = false; break; }
+          if (!warp_wait<true>(rf_smem_u32(&sm.bar_dq_done[h]), ph, abort)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) issue_s(t + 2);
+          __syncwarp();
+        }
+      }
+      if (!ok && lane == 0) record_timeout(abort, a.status, 6);
+      if (elect_one()) {
+        tc_commit(rf_smem_u32(&sm.bar_final));
+        tc_commit(rf_smem_u32(&sm.bar_drain));
+      }
+      __syncwarp();
+      volatile int no_abort = 0;
+      warp_wait(rf_smem_u32(&sm.bar_drain), 0, &no_abort);
+    }
+  } else {
+    // ---------------- dS and epilogue ----------------
+    const int e = warp >> 2, w = e & 1, h = e >> 1;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t scol = lane_base + 192 * h + 64 * w, acol = lane_base + 192 * h + 128;
+    const float* st = a.stats + ((size_t)n * g.t_qblk + tb) * (4 * RF_BLOCK);
+    const float nlse = st[w * RF_BLOCK + r];
+    const float c = (w == 0 ? 1.f : -a.lambda[n]) * (kBf16 ? 1.f : rf_pow2(es));
+    const float dc = c * st[(2 + w) * RF_BLOCK + r];
+    bool ok = true;
+    for (int b = 0; b < nv; ++b) {
+      if (!warp_wait(rf_smem_u32(&sm.bar_sd_full[h]), b & 1, abort)) { ok = false; break; }
+      tc_fence_after();
+      const int vr = (sm.list[b] == s.n_pb - 1) ? vr_last : RF_BLOCK;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t sr[32], da[32], pk[16];
+        tmem_ld32(scol + 32 * x, sr);
+        tmem_ld32(acol + 32 * x, da);
+        tmem_wait_ld();
+        if (vr == RF_BLOCK) ds_chunk<kBf16, true>(sr, da, 64 * h + 32 * x, vr, a.sl2, nlse, c, dc, pk);
+        else                ds_chunk<kBf16, false>(sr, da, 64 * h + 32 * x, vr, a.sl2, nlse, c, dc, pk);
+        tmem_st16(scol + 16 * x, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(rf_smem_u32(&sm.bar_ds_full[h]));
+    }
+    if (!ok) record_timeout(abort, a.status, 7);
+    const bool have = nv > 0 && !*abort && warp_wait(rf_smem_u32(&sm.bar_final), 0, abort) && !*abort;
+    if (have) tc_fence_after();
+    constexpr int kN = D / 4;  // columns each warpgroup writes
+    const int col = e * kN;
+    const uint32_t tcol = lane_base + kDq + (D == 128 ? col : 64 * (col >> 5) + col);
+    const float f = a.scale * (kBf16 ? 1.f : rf_pow2(-es));
+    store_row<kN, kBf16>(tcol, have, f, r < q_rows,
+                         a.dq + rf_row_offset(g, s, g.n1, n, q_r0 + min(r, q_rows - 1)) + col);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// dK and dV.  M = the block's 128 keys (thread = key = TMEM lane); a step is 64
+// query rows of one (head, query block) that lists the block: S_w^T and dA^T
+// with N = 64, A^T, dS_w^T from registers, then dV += A^T dO, dK_w += dS_w^T Q_w.
+// TMEM: dV at [256, 256 + D), dK at [384, 512) (per map 64 columns, as dQ), and
+// four 64-column slots in which a step's S_1, S_2 and dA take turns: A and dS_1
+// are written over S_1's slot and dS_2 over S_2's, each thread over columns that
+// it alone has read; S_1 of the next step goes into the free slot while this
+// step's elements are computed, its S_2 into dA's slot as soon as those are
+// done, and its dA into S_1's slot once A and dS_1 have been read.
+// Warpgroup e takes queries [16 e, +16) of the step, which is one 16-wide slice
+// of the reduction of dV and dK.
+// Rows that a query block does not have carry -lse = -inf (P = 0); their Q and
+// dO rows are zeroed in shared memory, so that nothing infinite meets that 0.
+// Bound: per 128 x 128 block and head the tensor pipe about 2,750 cycles, the
+// ex2 unit 2,048.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    rf_diff_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                       const __grid_constant__ BwdArgs a) {
+  using Smem = DkvSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  constexpr int kBoxes = D * 2 / 128;
+  constexpr uint32_t kTileBytes = Smem::kTileBytes;
+  constexpr uint32_t kDv = 256, kDk = 384;
+
+  const RfGeomDev& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gk = blockIdx.x / g.t_qblk, tb = blockIdx.x % g.t_qblk;  // tb: the key block
+  const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
+  const int group = g.n1 / g.n2;
+  int k_r0, k_rows;
+  rf_block_span(s, tb - s.qblk_off, k_r0, k_rows);
+  volatile int* abort = &sm.abort;
+  const bool bnsd = g.layout == RF_LAYOUT_BNSD;
+  auto coords = [&](int heads, int head, int r0, int& c1, int& c2) {
+    if (bnsd) { c1 = r0; c2 = s.batch_idx * heads + head; }
+    else      { c1 = head; c2 = (int)s.row_off + r0; }
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(rf_smem_u32(&sm.bar_kv), 1);
+    mbar_init(rf_smem_u32(&sm.bar_aux), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(rf_smem_u32(&sm.bar_full[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_empty[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_s1_full[i]), 1);
+    }
+    mbar_init(rf_smem_u32(&sm.bar_s2_full), 1);
+    mbar_init(rf_smem_u32(&sm.bar_da_full), 1);
+    mbar_init(rf_smem_u32(&sm.bar_ew), kCompute);
+    mbar_init(rf_smem_u32(&sm.bar_x_done), 1);
+    mbar_init(rf_smem_u32(&sm.bar_y_done), 1);
+    mbar_init(rf_smem_u32(&sm.bar_final), 1);
+    mbar_init(rf_smem_u32(&sm.bar_drain), 1);
+    sm.abort = 0;
+    sm.n_items = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(rf_smem_u32(&sm.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  // (head of the group, query block) pairs that list this key block
+  int mine = 0;
+  for (int i = threadIdx.x; i < group * a.words; i += kThreads) {
+    const int hh = i / a.words;
+    mine += __popc(a.bits[((size_t)(gk * group + hh) * g.t_qblk + tb) * a.words + (i - hh * a.words)]);
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0 && mine) atomicAdd(&sm.n_items, mine);
+  const bool stopped = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT) != 0;
+  tc_fence_before();
+  const int any_stopped = __syncthreads_or(stopped ? 1 : 0);
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  const int ni = any_stopped ? 0 : sm.n_items;
+  int ea, es;
+  carry_exponents<D, kBf16>(a.amax, ea, es);
+
+  if (warp >= 16) {
+    if (warp == kLoadWarp && ni > 0) {
+      // ---------------- loads: K and V once, then Q, dO and the rows' numbers per item ----------------
+      volatile int no_abort = 0;
+      int c1, c2;
+      if (lane == 0) {
+        coords(g.n2, gk, k_r0, c1, c2);
+        mbar_arrive_expect_tx(rf_smem_u32(&sm.bar_kv), 2 * kTileBytes);
+        for (int x = 0; x < kBoxes; ++x) {
+          tma_load_3d(rf_smem_u32(sm.k + x * kBoxBytes), &tm_k, rf_smem_u32(&sm.bar_kv), x * 64, c1, c2);
+          tma_load_3d(rf_smem_u32(sm.v + x * kBoxBytes), &tm_v, rf_smem_u32(&sm.bar_kv), x * 64, c1, c2);
+        }
+      }
+      __syncwarp();
+      int it = 0, tails = 0;
+      bool ok = true;
+      for (int hh = 0; ok && hh < group; ++hh) {
+        const int n = gk * group + hh;
+        const float lam = a.lambda[n];
+        const uint32_t* bw = a.bits + ((size_t)n * g.t_qblk + tb) * a.words;
+        for (int wd = 0; ok && wd < a.words; ++wd) {
+          uint32_t word = bw[wd];
+          while (word) {
+            const int qb = wd * 32 + __ffs(word) - 1;
+            word &= word - 1;
+            const int st = it & 1;
+            if (it >= 2 && !warp_wait(rf_smem_u32(&sm.bar_empty[st]), ((it >> 1) & 1) ^ 1, abort)) {
+              if (lane == 0) record_timeout(abort, a.status, 8);
+              ok = false;
+              break;
+            }
+            int r0, nr;
+            rf_block_span(s, qb, r0, nr);
+            const bool tail = nr < RF_BLOCK;
+            const uint32_t bar = rf_smem_u32(tail ? &sm.bar_aux : &sm.bar_full[st]);
+            if (lane == 0) {
+              sm.lam[st] = lam;
+              coords(g.n1, n, r0, c1, c2);
+              mbar_arrive_expect_tx(bar, 2 * kTileBytes + kStatBytes);
+              for (int x = 0; x < kBoxes; ++x) {
+                tma_load_3d(rf_smem_u32(sm.q[st] + x * kBoxBytes), &tm_q, bar, x * 64, c1, c2);
+                tma_load_3d(rf_smem_u32(sm.d_o[st] + x * kBoxBytes), &tm_do, bar, x * 64, c1, c2);
+              }
+              bulk_load(rf_smem_u32(&sm.stats[st][0][0]),
+                        a.stats + ((size_t)n * g.t_qblk + s.qblk_off + qb) * (4 * RF_BLOCK), kStatBytes, bar);
+            }
+            __syncwarp();
+            if (tail) {  // at most one query block per head
+              const bool landed = warp_wait(bar, tails & 1, &no_abort);
+              ++tails;
+              if (landed) {
+                zero_tail(sm.q[st], kBoxes, nr, lane);
+                zero_tail(sm.d_o[st], kBoxes, nr, lane);
+              }
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (!landed) record_timeout(abort, a.status, 8);
+                mbar_arrive(rf_smem_u32(&sm.bar_full[st]));
+              }
+              __syncwarp();
+            }
+            ++it;
+          }
+        }
+      }
+      if (*abort) {
+        warp_wait(rf_smem_u32(&sm.bar_kv), 0, &no_abort);
+        for (int i = (it > 2 ? it - 2 : 0); i < it; ++i)
+          warp_wait(rf_smem_u32(&sm.bar_full[i & 1]), (i >> 1) & 1, &no_abort);
+      }
+    } else if (warp == kMmaWarp && ni > 0) {
+      // ---------------- tcgen05.mma issue ----------------
+      const uint32_t fmt = kBf16 ? 1u : 0u;
+      const uint32_t id_s = umma_idesc_f16(fmt, 128, 64, 0);
+      const uint32_t id_dk = umma_idesc_f16(fmt, 128, 64, 1);
+      const uint32_t id_dv = umma_idesc_f16(fmt, 128, D, 1);
+      const uint64_t dk = umma_desc_sw128(rf_smem_u32(sm.k), 16, 1024);
+      const uint64_t dv = umma_desc_sw128(rf_smem_u32(sm.v), 16, 1024);
+      const uint64_t dq0 = umma_desc_sw128(rf_smem_u32(sm.q[0]), 16, 1024);
+      const uint64_t do0 = umma_desc_sw128(rf_smem_u32(sm.d_o[0]), 16, 1024);
+      const uint64_t dqn0 = umma_desc_sw128(rf_smem_u32(sm.q[0]), kBoxBytes, 1024);
+      const uint64_t don0 = umma_desc_sw128(rf_smem_u32(sm.d_o[0]), kBoxBytes, 1024);
+      const int nt = 2 * ni;
+      // slots of step t: S_1, S_2, dA (the fourth is free for the next S_1)
+      auto slot = [&](int t, int which) -> uint32_t {
+        const uint32_t tab = which == 0 ? 0x2130u : (which == 1 ? 0x3021u : 0x1302u);
+        return tmem + 64u * ((tab >> (4 * (t & 3))) & 15u);
+      };
+      auto tile_off = [&](int t) -> uint64_t {  // stage and 64-row half of step t's Q and dO
+        return (uint64_t)((((t >> 1) & 1) * kTileBytes + (t & 1) * kHalf) >> 4);
+      };
+      auto issue_s = [&](int t, int w) {
+        const uint64_t b = dq0 + tile_off(t);
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) {
+          const int byte = w * D + kk * 32;
+          const uint32_t off = ((uint32_t)(byte >> 7) * kBoxBytes + (byte & 127)) >> 4;
+          mma_ss(slot(t, w), dk + off, b + off, id_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(rf_smem_u32(w == 0 ? &sm.bar_s1_full[t & 1] : &sm.bar_s2_full));
+      };
+      auto issue_da = [&](int t) {
+        const uint64_t b = do0 + tile_off(t);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+          mma_ss(slot(t, 2), dv + off, b + off, id_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(rf_smem_u32(&sm.bar_da_full));
+      };
+      bool ok = warp_wait<true>(rf_smem_u32(&sm.bar_kv), 0, abort) &&
+                warp_wait<true>(rf_smem_u32(&sm.bar_full[0]), 0, abort);
+      if (ok) {
+        tc_fence_after();
+        if (elect_one()) {
+          issue_s(0, 0);
+          issue_s(0, 1);
+          issue_da(0);
+        }
+        __syncwarp();
+      }
+      for (int t = 0; ok && t < nt; ++t) {
+        const bool more = t + 1 < nt;
+        if (more) {
+          const int it1 = (t + 1) >> 1;
+          if (((t + 1) & 1) == 0 &&
+              !warp_wait<true>(rf_smem_u32(&sm.bar_full[it1 & 1]), (it1 >> 1) & 1, abort)) { ok = false; break; }
+          // the slot of S_1(t + 1) held dS_2(t - 1)
+          if (t > 0 && !warp_wait<true>(rf_smem_u32(&sm.bar_y_done), (t - 1) & 1, abort)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) issue_s(t + 1, 0);
+          __syncwarp();
+        }
+        if (!warp_wait<true>(rf_smem_u32(&sm.bar_ew), t & 1, abort)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          if (more) issue_s(t + 1, 1);
+          const uint64_t bo = don0 + tile_off(t), bq = dqn0 + tile_off(t);
+          const uint32_t sa = slot(t, 0), sb = slot(t, 1);
+          const uint32_t acc = t > 0 ? 1u : 0u;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(tmem + kDv, sa + 16 * kk, bo + (uint64_t)(kk * 2048 >> 4), id_dv, kk > 0 ? 1u : acc);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(tmem + kDk, sa + 16 * kk + 8, bq + (uint64_t)(kk * 2048 >> 4), id_dk, kk > 0 ? 1u : acc);
+          tc_commit(rf_smem_u32(&sm.bar_x_done));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(tmem + kDk + 64, sb + 16 * kk,
+                   bq + (uint64_t)(((D == 128 ? 1 : 0) * kBoxBytes + kk * 2048) >> 4), id_dk, kk > 0 ? 1u : acc);
+          tc_commit(rf_smem_u32(&sm.bar_y_done));
+          if (t & 1) tc_commit(rf_smem_u32(&sm.bar_empty[(t >> 1) & 1]));
+        }
+        __syncwarp();
+        if (more) {
+          // the slot of dA(t + 1) held A(t) and dS_1(t)
+          if (!warp_wait<true>(rf_smem_u32(&sm.bar_x_done), t & 1, abort)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) issue_da(t + 1);
+          __syncwarp();
+        }
+      }
+      if (!ok && lane == 0) record_timeout(abort, a.status, 9);
+      if (elect_one()) {
+        tc_commit(rf_smem_u32(&sm.bar_final));
+        tc_commit(rf_smem_u32(&sm.bar_drain));
+      }
+      __syncwarp();
+      volatile int no_abort = 0;
+      warp_wait(rf_smem_u32(&sm.bar_drain), 0, &no_abort);
+    }
+  } else {
+    // ---------------- A, dS and epilogue ----------------
+    const int e = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint64_t sl = rf_f2(__float_as_uint(a.sl2), __float_as_uint(a.sl2));
+    const float up_a = (float)ea, up_s = kBf16 ? 1.f : rf_scale_pow2(1.f, es - ea);
+    bool ok = true;
+    for (int t = 0; t < 2 * ni; ++t) {
+      const uint32_t ta = 0x2130u, tbb = 0x3021u, tc = 0x1302u;
+      const uint32_t s1c = lane_base + 64u * ((ta >> (4 * (t & 3))) & 15u) + 16 * e;
+      const uint32_t s2c = lane_base + 64u * ((tbb >> (4 * (t & 3))) & 15u) + 16 * e;
+      const uint32_t dac = lane_base + 64u * ((tc >> (4 * (t & 3))) & 15u) + 16 * e;
+      const int st = (t >> 1) & 1, q0 = 64 * (t & 1) + 16 * e;
+      // the item's numbers are visible: its tiles' barrier is the same
+      if ((t & 1) == 0 && !warp_wait(rf_smem_u32(&sm.bar_full[st]), (t >> 2) & 1, abort)) { ok = false; break; }
+      if (!warp_wait(rf_smem_u32(&sm.bar_s1_full[t & 1]), (t >> 1) & 1, abort)) { ok = false; break; }
+      if (!warp_wait(rf_smem_u32(&sm.bar_s2_full), t & 1, abort)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t s1[16], s2[16];
+      tmem_ld16(s1c, s1);
+      tmem_ld16(s2c, s2);
+      tmem_wait_ld();
+      const float nlam = -sm.lam[st];
+      const uint64_t nl2 = rf_f2(__float_as_uint(nlam), __float_as_uint(nlam));
+      const uint64_t ua = rf_f2(__float_as_uint(up_a), __float_as_uint(up_a));
+      const uint64_t us = rf_f2(__float_as_uint(up_s), __float_as_uint(up_s));
+      uint32_t out[16];  // A in [0, 8), dS_1 in [8, 16)
+      uint32_t out2[8];
+      const float* l1 = sm.stats[st][0] + q0;
+      const float* l2 = sm.stats[st][1] + q0;
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        uint64_t x = rf_fma2(rf_f2(s1[i], s1[i + 1]), sl, *reinterpret_cast<const uint64_t*>(l1 + i));
+        uint64_t y = rf_fma2(rf_f2(s2[i], s2[i + 1]), sl, *reinterpret_cast<const uint64_t*>(l2 + i));
+        if constexpr (!kBf16) {
+          x = rf_add2(x, ua);
+          y = rf_add2(y, ua);
+        }
+        float x0, x1, y0, y1;
+        rf_f2_split(x, x0, x1);
+        rf_f2_split(y, y0, y1);
+        const uint64_t p1 = rf_f2(__float_as_uint(rf_ex2(x0)), __float_as_uint(rf_ex2(x1)));
+        const uint64_t p2 = rf_mul2(nl2, rf_f2(__float_as_uint(rf_ex2(y0)), __float_as_uint(rf_ex2(y1))));
+        float a0, a1;
+        rf_f2_split(rf_add2(p1, p2), a0, a1);
+        out[i >> 1] = rf_pack2<kBf16>(a0, a1);
+        rf_f2_split(p1, x0, x1);
+        rf_f2_split(p2, y0, y1);
+        s1[i] = __float_as_uint(x0);
+        s1[i + 1] = __float_as_uint(x1);
+        s2[i] = __float_as_uint(y0);
+        s2[i + 1] = __float_as_uint(y1);
+      }
+      if (!warp_wait(rf_smem_u32(&sm.bar_da_full), t & 1, abort)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t da[16];
+      tmem_ld16(dac, da);
+      tmem_wait_ld();
+      const float* d1 = sm.stats[st][2] + q0;
+      const float* d2 = sm.stats[st][3] + q0;
+      const uint64_t neg1 = rf_f2(__float_as_uint(-1.f), __float_as_uint(-1.f));
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const uint64_t dd = rf_f2(da[i], da[i + 1]);
+        uint64_t t1 = rf_fma2(*reinterpret_cast<const uint64_t*>(d1 + i), neg1, dd);
+        uint64_t t2 = rf_fma2(*reinterpret_cast<const uint64_t*>(d2 + i), neg1, dd);
+        if constexpr (!kBf16) {
+          t1 = rf_mul2(t1, us);
+          t2 = rf_mul2(t2, us);
+        }
+        float y0, y1;
+        rf_f2_split(rf_mul2(rf_f2(s1[i], s1[i + 1]), t1), y0, y1);
+        out[8 + (i >> 1)] = rf_pack2<kBf16>(y0, y1);
+        rf_f2_split(rf_mul2(rf_f2(s2[i], s2[i + 1]), t2), y0, y1);
+        out2[i >> 1] = rf_pack2<kBf16>(y0, y1);
+      }
+      tmem_st16(s1c, out);
+      tmem_st8(s2c, out2);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(rf_smem_u32(&sm.bar_ew));
+    }
+    if (!ok) record_timeout(abort, a.status, 10);
+    const bool have = ni > 0 && !*abort && warp_wait(rf_smem_u32(&sm.bar_final), 0, abort) && !*abort;
+    if (have) tc_fence_after();
+    constexpr int kN = D / 4;
+    const int col = e * kN;
+    const size_t off = rf_row_offset(g, s, g.n2, gk, k_r0 + min(r, k_rows - 1)) + col;
+    const bool live = r < k_rows;
+    store_row<kN, kBf16>(lane_base + kDv + col, have, kBf16 ? 1.f : rf_pow2(-ea), live, a.dv + off);
+    store_row<kN, kBf16>(lane_base + kDk + (D == 128 ? col : 64 * (col >> 5) + col), have,
+                         a.scale * (kBf16 ? 1.f : rf_pow2(-es)), live, a.dk + off);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Per (query block, head): packs each row's -lse_1, -lse_2, delta_1 and delta_2
+// (rows the block does not have: -inf, -inf, 0, 0), sums delta_2 over the
+// block's rows in a fixed order, and sets this query block's bit for every key
+// block it lists.  fp16: also the largest finite |dO|, |V| and |lambda|
+// (CTAs past t_qblk * n1 read V).  HBM-bound: 10 D bytes per row and head.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(256)
+    rf_diff_prep_bwd_kernel(const __grid_constant__ RfGeomDev g, const int32_t* __restrict__ sel_idx,
+                            const int32_t* __restrict__ sel_num, const float* __restrict__ lambda,
+                            const uint16_t* __restrict__ d_o, const uint16_t* __restrict__ v,
+                            const float* __restrict__ maps, const float* __restrict__ lse, long long rows_total,
+                            int words, float* __restrict__ stats, uint32_t* __restrict__ bits,
+                            float* __restrict__ dlam, uint32_t* __restrict__ amax, uint32_t* __restrict__ status) {
+  __shared__ int list[RF_MAX_KV_LIST];
+  __shared__ float part[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kPer = D / 32;  // columns per lane
+  const bool is_v = (int)blockIdx.x >= g.t_qblk * g.n1;
+  const int bid = is_v ? (int)blockIdx.x - g.t_qblk * g.n1 : (int)blockIdx.x;
+  const int n = bid / g.t_qblk, tb = bid % g.t_qblk;
+  const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
+  const int lq = tb - s.qblk_off;
+  int r0, nrows;
+  rf_block_span(s, lq, r0, nrows);
+  auto decode = [](uint32_t u) { return kBf16 ? __uint_as_float(u << 16) : __half2float(__ushort_as_half((unsigned short)u)); };
+  float top = 0.f;
+  auto finite_max = [&](float x) {
+    const float m = fabsf(x);
+    if (m < INFINITY) top = fmaxf(top, m);
+  };
+  if (is_v) {
+    for (int r = warp; r < nrows; r += 8) {
+      const uint16_t* p = v + rf_row_offset(g, s, g.n2, n, r0 + r) + lane * kPer;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) finite_max(decode(p[c]));
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if (lane == 0) atomicMax(amax + 1, __float_as_uint(top));
+    return;
+  }
+  const size_t row_id = (size_t)tb * g.n1 + n;
+  const int num_raw = sel_num[row_id];
+  const int num = num_raw < 0 ? 0 : (num_raw > g.max_kv ? g.max_kv : num_raw);
+  for (int c = threadIdx.x; c < num; c += 256) list[c] = sel_idx[row_id * g.max_kv + c];
+  __syncthreads();
+  float* st = stats + ((size_t)n * g.t_qblk + tb) * (4 * RF_BLOCK);
+  const size_t map2 = (size_t)rows_total * g.n1 * D;
+  const size_t lrow = (g.layout == RF_LAYOUT_BNSD ? (size_t)s.batch_idx * s.L : (size_t)s.row_off) + r0;
+  float sum2 = 0.f;
+  for (int r = warp; r < RF_BLOCK; r += 8) {
+    float e1 = 0.f, e2 = 0.f;
+    if (r < nrows) {
+      const size_t off = rf_row_offset(g, s, g.n1, n, r0 + r) + lane * kPer;
+      uint16_t u[kPer];
+      float m1[kPer], m2[kPer];
+      if constexpr (kPer == 4) {
+        *reinterpret_cast<uint2*>(u) = *reinterpret_cast<const uint2*>(d_o + off);
+        *reinterpret_cast<float4*>(m1) = *reinterpret_cast<const float4*>(maps + off);
+        *reinterpret_cast<float4*>(m2) = *reinterpret_cast<const float4*>(maps + map2 + off);
+      } else {
+        *reinterpret_cast<uint32_t*>(u) = *reinterpret_cast<const uint32_t*>(d_o + off);
+        *reinterpret_cast<float2*>(m1) = *reinterpret_cast<const float2*>(maps + off);
+        *reinterpret_cast<float2*>(m2) = *reinterpret_cast<const float2*>(maps + map2 + off);
+      }
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        const float x = decode(u[c]);
+        e1 = fmaf(x, m1[c], e1);
+        e2 = fmaf(x, m2[c], e2);
+        if constexpr (!kBf16) finite_max(x);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        e1 += __shfl_xor_sync(0xffffffffu, e1, d);
+        e2 += __shfl_xor_sync(0xffffffffu, e2, d);
+      }
+    }
+    sum2 += e2;
+    if (lane == 0) {
+      st[r] = r < nrows ? -lse[(size_t)n * rows_total + lrow + r] : -INFINITY;
+      st[RF_BLOCK + r] = r < nrows ? -lse[((size_t)g.n1 + n) * rows_total + lrow + r] : -INFINITY;
+      st[2 * RF_BLOCK + r] = e1;
+      st[3 * RF_BLOCK + r] = e2;
+    }
+  }
+  if (lane == 0) part[warp] = sum2;
+  if constexpr (!kBf16) {
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if (lane == 0) atomicMax(amax, __float_as_uint(top));
+    if (threadIdx.x == 0 && fabsf(lambda[n]) < INFINITY) atomicMax(amax + 2, __float_as_uint(fabsf(lambda[n])));
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += part[i];
+    dlam[(size_t)n * g.t_qblk + tb] = sum;
+  }
+  if (warp == 0) {
+    int bad = (lane == 0 && num != num_raw) ? 1 : 0;
+    const int cnt = compact_ascending(list, num, s.n_pb + s.nb, lane, &bad);
+    bad = __reduce_add_sync(0xffffffffu, bad);
+    if (lane == 0 && bad) atomicAdd(status + RF_STATUS_BAD_INDEX, (uint32_t)bad);
+    for (int c = lane; c < cnt; c += 32)
+      atomicOr(bits + ((size_t)n * g.t_qblk + s.qblk_off + list[c]) * words + (lq >> 5), 1u << (lq & 31));
+  }
+}
+
+// dlambda[n] = -sum over the query blocks of their sums of delta_2, in a fixed order.
+__global__ void __launch_bounds__(256) rf_diff_dlam_kernel(const float* __restrict__ part, int t_qblk,
+                                                           float* __restrict__ dlambda) {
+  __shared__ float red[8];
+  float sum = 0.f;
+  for (int i = threadIdx.x; i < t_qblk; i += 256) sum += part[(size_t)blockIdx.x * t_qblk + i];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) sum += red[i];
+    dlambda[blockIdx.x] = -sum;
+  }
+}
+
+template <int D, bool kBf16>
+rf_status_t launch_t(const rf_plan* p, const BwdArgs& a, const void* q_r, const void* k_r, const void* v_r,
+                     const void* do_r, const float* maps, const float* lse, float* stats, uint32_t* bits,
+                     float* dlam_part, uint32_t* amax, float* dlambda, cudaStream_t st) {
+  const RfGeomDev& g = p->g;
+  const long long gq = (long long)g.t_qblk * g.n1, gkv = (long long)g.t_qblk * g.n2;
+  if (gq + gkv > 0x7FFFFFFFll) return rf_fail(RF_ERR_INVALID_ARG, "grid too large");
+  CUtensorMap mq, mk, mv, mo;
+  rf_status_t s;
+  if ((s = make_map(&mq, p, q_r, g.n1, kElemPlan)) != RF_OK) return s;
+  if ((s = make_map(&mk, p, k_r, g.n2, kElemPlan)) != RF_OK) return s;
+  if ((s = make_map(&mv, p, v_r, g.n2, kElemPlan)) != RF_OK) return s;
+  if ((s = make_map(&mo, p, do_r, g.n1, kElemPlan)) != RF_OK) return s;
+  size_t sq = sizeof(DqSmem<D>) + 1024, skv = sizeof(DkvSmem<D>) + 1024;
+  if (sq < 120 * 1024) sq = 120 * 1024;    // each CTA takes all 512 TMEM columns: one per SM
+  if (skv < 120 * 1024) skv = 120 * 1024;
+  auto kq = rf_diff_dq_kernel<D, kBf16>;
+  auto kkv = rf_diff_dkv_kernel<D, kBf16>;
+  if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sq) != cudaSuccess ||
+      cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)skv) != cudaSuccess)
+    return rf_check_launch("cudaFuncSetAttribute(rf_diff backward)");
+  // one memset: the bit rows, dlambda's parts and amax lie together
+  if (cudaMemsetAsync(bits, 0, (size_t)((char*)amax - (char*)bits) + 256, st) != cudaSuccess)
+    return rf_check_launch("cudaMemsetAsync(rf_diff backward)");
+  const unsigned prep = (unsigned)(gq + (kBf16 ? 0 : gkv));
+  rf_diff_prep_bwd_kernel<D, kBf16><<<prep, 256, 0, st>>>(
+      g, a.sel_idx, a.sel_num, a.lambda, static_cast<const uint16_t*>(do_r), static_cast<const uint16_t*>(v_r), maps,
+      lse, p->rows_total, a.words, stats, bits, dlam_part, amax, a.status);
+  if ((s = rf_check_launch("rf_diff_prep_bwd_kernel")) != RF_OK) return s;
+  rf_diff_dlam_kernel<<<(unsigned)g.n1, 256, 0, st>>>(dlam_part, g.t_qblk, dlambda);
+  if ((s = rf_check_launch("rf_diff_dlam_kernel")) != RF_OK) return s;
+  kkv<<<(unsigned)gkv, kThreads, skv, st>>>(mq, mk, mv, mo, a);
+  if ((s = rf_check_launch("rf_diff_dkv_kernel")) != RF_OK) return s;
+  kq<<<(unsigned)gq, kThreads, sq, st>>>(mq, mk, mv, mo, a);
+  return rf_check_launch("rf_diff_dq_kernel");
+}
+
+}  // namespace
+
+rf_status_t rf_launch_diff_bwd(const rf_plan* p, const void* q_r, const void* k_r, const void* v_r,
+                               const int32_t* sel_idx, const int32_t* sel_num, const float* lambda,
+                               float scale, const float* maps, const float* lse, const void* do_r,
+                               void* dq_r, void* dk_r, void* dv_r, float* dlambda, void* ws,
+                               cudaStream_t st) {
+  const RfDiffLayout lay = rf_diff_layout(p);
+  char* w = static_cast<char*>(ws);
+  float* stats = reinterpret_cast<float*>(w + lay.stats);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(w + lay.bits);
+  float* part = reinterpret_cast<float*>(w + lay.dlam);
+  uint32_t* amax = reinterpret_cast<uint32_t*>(w + lay.amax);
+  BwdArgs a;
+  a.g = p->g;
+  a.sel_idx = sel_idx;
+  a.sel_num = sel_num;
+  a.lambda = lambda;
+  a.stats = stats;
+  a.bits = bits;
+  a.amax = amax;
+  a.words = lay.words;
+  a.dq = static_cast<uint16_t*>(dq_r);
+  a.dk = static_cast<uint16_t*>(dk_r);
+  a.dv = static_cast<uint16_t*>(dv_r);
+  a.status = reinterpret_cast<uint32_t*>(w + p->off_status);
+  a.scale = scale;
+  a.sl2 = scale * kLog2e;
+  const bool bf = p->dtype == RF_BF16;
+  if (p->g.d == 128)
+    return bf ? launch_t<128, true>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, amax, dlambda, st)
+              : launch_t<128, false>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, amax, dlambda, st);
+  return bf ? launch_t<64, true>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, amax, dlambda, st)
+            : launch_t<64, false>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, amax, dlambda, st);
+}

@@ -71,6 +71,21 @@ struct rf_plan {
   int64_t kept_flops_upper;
 };
 
+// Workspace regions of the differential-attention calls (byte offsets), behind
+// the plan's own workspace.
+struct RfDiffLayout {
+  int64_t v16;        // f16 copies of V' by block, [n2][t_qblk][128][d], rows past a block's end zero
+  int64_t v_exp;      // int32 [n2][t_qblk]: block t of V' is v16 * 2^v_exp
+  int64_t end_serve;  // what rf_diff_attn needs ends here
+  int64_t stats;      // float4 {lse_1, lse_2, delta_1, delta_2} per row, [n1][t_qblk][128]
+  int64_t bits;       // query blocks that list a key block: uint32 [n1][t_qblk][words]
+  int64_t dlam;       // per-block sums of dO . O_2, fp32 [n1][t_qblk]
+  int64_t amax;       // uint32 {largest |dO|, largest |V|} as fp32 bits (fp16 plans)
+  int64_t end;        // what rf_diff_attn_backward needs ends here
+  int words;          // 32-bit words of one bit row: ceil(longest sequence's blocks / 32)
+};
+RfDiffLayout rf_diff_layout(const rf_plan* p);
+
 // Status words at the start of the workspace.
 enum { RF_STATUS_BAD_INDEX = 0, RF_STATUS_TIMEOUT = 1, RF_STATUS_WORDS = 64 };
 
@@ -96,3 +111,14 @@ rf_status_t rf_launch_exp2_selftest(const float* x, float* y_poly, float* y_mufu
 rf_status_t rf_launch_attn(const rf_plan* p, const void* q_r, const void* k_r, const void* v_r,
                            const int32_t* sel_idx, const int32_t* sel_num, float scale,
                            void* o_r, void* ws, cudaStream_t st);
+rf_status_t rf_launch_diff_attn(const rf_plan* p, const void* q_r, const void* k_r, const void* v_r,
+                                const int32_t* sel_idx, const int32_t* sel_num, const float* lambda,
+                                float scale, void* o_r, float* maps, float* lse, void* ws,
+                                cudaStream_t st);
+rf_status_t rf_launch_diff_bwd(const rf_plan* p, const void* q_r, const void* k_r, const void* v_r,
+                               const int32_t* sel_idx, const int32_t* sel_num, const float* lambda,
+                               float scale, const float* maps, const float* lse, const void* do_r,
+                               void* dq_r, void* dk_r, void* dv_r, float* dlambda, void* ws,
+                               cudaStream_t st);
+rf_status_t rf_launch_gather(const rf_plan* p, int heads, const void* x, void* x_r, bool inverse,
+                             cudaStream_t st);

@@ -1,0 +1,700 @@
+// Group norm with an activation over channels-last rows, forward and backward.
+//
+//   mu, var: mean and variance of x over a group's channels, of one row
+//            (RF_NORM_ROW: each head of an attention output on its own) or of
+//            all rows of a batch element (RF_NORM_SAMPLE)
+//   xh = (x - mu) / sqrt(var + eps),  z = gamma xh + beta,  y = act(z)
+// and with g = dy act'(z):
+//   dgamma = sum g xh,  dbeta = sum g  over the rows,
+//   dx = (gamma g - mean(gamma g) - xh mean(gamma g xh)) / sqrt(var + eps).
+// Everything is computed in fp32 and rounded once.  Means and variances are
+// taken about a value of the data (two-pass in registers for rows; for samples
+// sums of x - x_0 per channel and slice, merged by the parallel-variance
+// formula), so that a mean far from zero does not cancel the variance away.
+// All sums run in a fixed order; there are no atomics.
+//
+// Bound: HBM.  A row's group is held in registers, so RF_NORM_ROW moves each
+// element once; RF_NORM_SAMPLE reads x twice (the second time from L2 where it
+// fits).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <string>
+
+#include "rf_device.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRowWidth = 1024;  // widest group held in one warp's registers
+
+struct NormArgs {
+  const void* x;
+  const void* gamma;
+  const void* beta;
+  const void* dy;
+  void* y;        // forward: y; backward: dx
+  float* stats;   // RF_NORM_SAMPLE: {mean, 1 / sqrt(var + eps)} per (batch, group)
+  float* ws;
+  long long rows, n_rows;            // rows per batch element, of all
+  long long xs_b, xs_r, xs_g, ys_b, ys_r, ys_g;
+  int batch, groups, width, pdt, act;
+  int slices;                        // row slices (partial sums) per batch element or of all rows
+  float eps;
+};
+
+__device__ __forceinline__ float load_p(const void* p, int dt, long long i) {
+  if (dt == RF_FP32) return static_cast<const float*>(p)[i];
+  if (dt == RF_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void store_p(void* p, int dt, long long i, float v) {
+  if (dt == RF_FP32) static_cast<float*>(p)[i] = v;
+  else if (dt == RF_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <class T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// VEC elements (16 bytes when VEC > 1) to and from fp32.
+template <class T, int VEC>
+__device__ __forceinline__ void load_v(const T* p, float* f) {
+  if constexpr (VEC == 1) {
+    f[0] = to_f(*p);
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const T* t = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = to_f(t[i]);
+  }
+}
+template <class T, int VEC>
+__device__ __forceinline__ void store_v(T* p, const float* f) {
+  if constexpr (VEC == 1) {
+    *p = from_f<T>(f[0]);
+  } else {
+    uint4 u;
+    T* t = reinterpret_cast<T*>(&u);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) t[i] = from_f<T>(f[i]);
+    *reinterpret_cast<uint4*>(p) = u;
+  }
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+__device__ __forceinline__ float act_f(float z, int act) { return act == RF_ACT_SILU ? z * sigmoid(z) : z; }
+// derivative of the activation at z
+__device__ __forceinline__ float act_d(float z, int act) {
+  if (act != RF_ACT_SILU) return 1.f;
+  const float s = sigmoid(z);
+  return s * fmaf(z, 1.f - s, 1.f);
+}
+
+// Sum over the `lanes` (a power of two) neighbouring lanes of a sub-warp.
+__device__ __forceinline__ float sub_sum(float v, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// One row per sub-warp of `lanes` lanes, NV vectors of VEC channels per lane;
+// blockIdx.y = group, so that gamma, beta and (backward) the channels' sums stay
+// in registers over all rows of the CTA's slice.
+template <class T, int VEC, int NV, bool kBwd>
+__global__ void __launch_bounds__(kThreads) rf_norm_row_kernel(const __grid_constant__ NormArgs a, int lanes) {
+  constexpr int E = VEC * NV;
+  const int g = blockIdx.y, lane = threadIdx.x % lanes, sub = threadIdx.x / lanes, subs = kThreads / lanes;
+  const T* x = static_cast<const T*>(a.x);
+  const T* dy = static_cast<const T*>(a.dy);
+  T* y = static_cast<T*>(a.y);
+  float gm[E], bt[E], sg[kBwd ? E : 1], sb[kBwd ? E : 1];
+  bool have[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * lanes + lane) * VEC;
+    have[v] = c < a.width;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      gm[v * VEC + i] = have[v] ? load_p(a.gamma, a.pdt, (long long)g * a.width + c + i) : 0.f;
+      bt[v * VEC + i] = have[v] ? load_p(a.beta, a.pdt, (long long)g * a.width + c + i) : 0.f;
+      if constexpr (kBwd) sg[v * VEC + i] = sb[v * VEC + i] = 0.f;
+    }
+  }
+  const float inv = 1.0f / (float)a.width;
+  const long long per = (a.n_rows + a.slices - 1) / a.slices;
+  const long long first = (long long)blockIdx.x * per, last = min(a.n_rows, first + per);
+  // every lane of a warp runs the same number of turns (the sums use the whole warp)
+  for (long long base = first; base < last; base += subs) {
+    const long long i = base + sub;
+    const bool live = i < last;
+    const long long ii = live ? i : last - 1;
+    const long long b = ii / a.rows, r = ii - b * a.rows;
+    const long long xo = b * a.xs_b + r * a.xs_r + g * a.xs_g, yo = b * a.ys_b + r * a.ys_r + g * a.ys_g;
+    float xv[E], dv[kBwd ? E : 1];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (have[v]) {
+        load_v<T, VEC>(x + xo + (v * lanes + lane) * VEC, xv + v * VEC);
+        if constexpr (kBwd) load_v<T, VEC>(dy + yo + (v * lanes + lane) * VEC, dv + v * VEC);
+      } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          xv[v * VEC + k] = 0.f;
+          if constexpr (kBwd) dv[v * VEC + k] = 0.f;
+        }
+      }
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) s += xv[k];
+    const float mu = sub_sum(s, lanes) * inv;
+    s = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int k = v * VEC; k < (v + 1) * VEC; ++k) {
+        xv[k] = have[v] ? xv[k] - mu : 0.f;
+        s = fmaf(xv[k], xv[k], s);
+      }
+    const float rstd = rsqrtf(sub_sum(s, lanes) * inv + a.eps);
+    if constexpr (!kBwd) {
+#pragma unroll
+      for (int k = 0; k < E; ++k) xv[k] = act_f(fmaf(xv[k] * rstd, gm[k], bt[k]), a.act);
+    } else {
+      float m1 = 0.f, m2 = 0.f;
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        xv[k] *= rstd;
+        const float gz = dv[k] * act_d(fmaf(xv[k], gm[k], bt[k]), a.act);
+        if (live) {
+          sg[k] = fmaf(gz, xv[k], sg[k]);
+          sb[k] += gz;
+        }
+        dv[k] = gz * gm[k];
+        m1 += dv[k];
+        m2 = fmaf(dv[k], xv[k], m2);
+      }
+      m1 = sub_sum(m1, lanes) * inv;
+      m2 = sub_sum(m2, lanes) * inv;
+#pragma unroll
+      for (int k = 0; k < E; ++k) xv[k] = rstd * (dv[k] - m1 - xv[k] * m2);
+    }
+    if (live) {
+      const long long oo = kBwd ? xo : yo;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (have[v]) store_v<T, VEC>(y + oo + (v * lanes + lane) * VEC, xv + v * VEC);
+    }
+  }
+  if constexpr (kBwd) {
+    // this CTA's sums per channel: sub-warps in order, through shared memory
+    __shared__ float red[2][kMaxRowWidth];
+    for (int turn = 0; turn < subs; ++turn) {
+      if (sub == turn) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (have[v])
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+              const int c = (v * lanes + lane) * VEC + k;
+              red[0][c] = (turn ? red[0][c] : 0.f) + sg[v * VEC + k];
+              red[1][c] = (turn ? red[1][c] : 0.f) + sb[v * VEC + k];
+            }
+      }
+      __syncthreads();
+    }
+    const long long ch = (long long)a.groups * a.width;
+    for (int c = threadIdx.x; c < a.width; c += kThreads) {
+      float* w = a.ws + (long long)blockIdx.x * 2 * ch + (long long)g * a.width + c;
+      w[0] = red[0][c];
+      w[ch] = red[1][c];
+    }
+  }
+}
+
+// ---- statistics over a batch element's rows -------------------------------------
+
+// Channel vector `cv` of VEC channels: element offset of its first channel (a
+// vector never crosses a group unless the groups are contiguous).
+__device__ __forceinline__ long long chan_off(long long c, int width, long long sg) {
+  const long long g = c / width;
+  return g * sg + (c - g * width);
+}
+
+// Per-channel partial sums of one slice of rows.  Forward: {sum(x - x0) as a
+// mean, sum of squared deviations}; backward: {sum g, sum g xh}.  A thread owns
+// VEC channels; the block's row lanes are merged in order.
+template <class T, int VEC, bool kBwd>
+__global__ void __launch_bounds__(kThreads) rf_norm_partial_kernel(const __grid_constant__ NormArgs a, int tile) {
+  __shared__ float red[2][kThreads][VEC];
+  const int b = blockIdx.z;
+  const long long ch = (long long)a.groups * a.width;
+  const int lanes = kThreads / tile, rl = threadIdx.x / tile;
+  const long long c = ((long long)blockIdx.y * tile + threadIdx.x % tile) * VEC;
+  const bool live = rl < lanes && c < ch;
+  const long long per = (a.rows + a.slices - 1) / a.slices;
+  const long long first = (long long)blockIdx.x * per, last = min(a.rows, first + per);
+  float p0[VEC], p1[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) p0[k] = p1[k] = 0.f;
+  float n = 0.f;
+  if (live && first + rl < last) {
+    const T* x = static_cast<const T*>(a.x) + b * a.xs_b + chan_off(c, a.width, a.xs_g);
+    float x0[VEC], gm[VEC], bt[VEC], mu[VEC], rs[VEC];
+    if constexpr (!kBwd) {
+      load_v<T, VEC>(x + (first + rl) * a.xs_r, x0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const long long g = (c + k) / a.width;
+        gm[k] = load_p(a.gamma, a.pdt, c + k);
+        bt[k] = load_p(a.beta, a.pdt, c + k);
+        mu[k] = a.stats[2 * (b * (long long)a.groups + g)];
+        rs[k] = a.stats[2 * (b * (long long)a.groups + g) + 1];
+      }
+    }
+    const T* dy = static_cast<const T*>(a.dy) + (kBwd ? b * a.ys_b + chan_off(c, a.width, a.ys_g) : 0);
+#pragma unroll 4
+    for (long long r = first + rl; r < last; r += lanes) {
+      float xv[VEC];
+      load_v<T, VEC>(x + r * a.xs_r, xv);
+      if constexpr (!kBwd) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          const float d = xv[k] - x0[k];
+          p0[k] += d;
+          p1[k] = fmaf(d, d, p1[k]);
+        }
+        n += 1.f;
+      } else {
+        float dv[VEC];
+        load_v<T, VEC>(dy + r * a.ys_r, dv);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          const float xh = (xv[k] - mu[k]) * rs[k];
+          const float gz = dv[k] * act_d(fmaf(xh, gm[k], bt[k]), a.act);
+          p0[k] += gz;
+          p1[k] = fmaf(gz, xh, p1[k]);
+        }
+      }
+    }
+    if constexpr (!kBwd) {
+      const float in = 1.0f / n;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        p1[k] = fmaxf(p1[k] - p0[k] * p0[k] * in, 0.f);
+        p0[k] = x0[k] + p0[k] * in;
+      }
+    }
+  }
+  if (rl < lanes) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      red[0][threadIdx.x][k] = p0[k];
+      red[1][threadIdx.x][k] = p1[k];
+    }
+  }
+  __syncthreads();
+  if (rl == 0 && c < ch) {
+    const long long rows = last > first ? last - first : 0;
+    for (int l = 1; l < lanes; ++l) {
+      const float nl = (float)((rows - l + lanes - 1) / lanes > 0 && l < rows ? (rows - l + lanes - 1) / lanes : 0);
+      if (!kBwd && nl == 0.f) break;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const float q0 = red[0][threadIdx.x + l * tile][k], q1 = red[1][threadIdx.x + l * tile][k];
+        if constexpr (!kBwd) {
+          const float d = q0 - p0[k], t = nl / (n + nl);
+          p0[k] = fmaf(d, t, p0[k]);
+          p1[k] += q1 + d * d * n * t;
+        } else {
+          p0[k] += q0;
+          p1[k] += q1;
+        }
+      }
+      n += nl;
+    }
+    float* w = a.ws + ((long long)b * a.slices + blockIdx.x) * 2 * ch + c;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      w[k] = p0[k];
+      w[ch + k] = p1[k];
+    }
+  }
+}
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) s += red[i];
+  return s;
+}
+
+// Forward: a (batch, group)'s mean and 1 / sqrt(var + eps) from its channels'
+// slices.  Means first, deviations about the common mean after.
+__global__ void __launch_bounds__(kThreads) rf_norm_stats_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float red[kThreads / 32];
+  const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
+  const long long ch = (long long)a.groups * a.width;
+  const float* w = a.ws + (long long)b * a.slices * 2 * ch + (long long)g * a.width;
+  const long long per = (a.rows + a.slices - 1) / a.slices;
+  const float total = (float)a.rows * (float)a.width;
+  const long long items = (long long)a.slices * a.width;
+  auto count = [&](long long sl) { return (float)max(0ll, min(a.rows - sl * per, per)); };
+  const float ref = w[0];  // sums about a value of the data
+  float s = 0.f;
+  for (long long i = threadIdx.x; i < items; i += kThreads) {
+    const long long sl = i / a.width, c = i - sl * a.width;
+    const float n = count(sl);
+    if (n > 0.f) s = fmaf(n, w[sl * 2 * ch + c] - ref, s);
+  }
+  const float mu = ref + block_sum(s, red) / total;
+  s = 0.f;
+  for (long long i = threadIdx.x; i < items; i += kThreads) {
+    const long long sl = i / a.width, c = i - sl * a.width;
+    const float n = count(sl);
+    if (n > 0.f) {
+      const float d = w[sl * 2 * ch + c] - mu;
+      s += w[sl * 2 * ch + ch + c] + n * d * d;
+    }
+  }
+  const float var = block_sum(s, red) / total;
+  if (threadIdx.x == 0) {
+    a.stats[2 * blockIdx.x] = mu;
+    a.stats[2 * blockIdx.x + 1] = rsqrtf(var + a.eps);
+  }
+}
+
+// Backward: {mean(gamma g), mean(gamma g xh)} of a (batch, group), behind the
+// slices' sums in the workspace.
+__global__ void __launch_bounds__(kThreads) rf_norm_means_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float red[kThreads / 32];
+  const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
+  const long long ch = (long long)a.groups * a.width;
+  const float* w = a.ws + (long long)b * a.slices * 2 * ch + (long long)g * a.width;
+  const float inv = 1.0f / ((float)a.rows * (float)a.width);
+  const long long items = (long long)a.slices * a.width;
+  float s0 = 0.f, s1 = 0.f;
+  for (long long i = threadIdx.x; i < items; i += kThreads) {
+    const long long sl = i / a.width, c = i - sl * a.width;
+    const float gm = load_p(a.gamma, a.pdt, (long long)g * a.width + c);
+    s0 = fmaf(gm, w[sl * 2 * ch + c], s0);
+    s1 = fmaf(gm, w[sl * 2 * ch + ch + c], s1);
+  }
+  s0 = block_sum(s0, red);
+  s1 = block_sum(s1, red);
+  if (threadIdx.x == 0) {
+    float* m = a.ws + (long long)a.batch * a.slices * 2 * ch + 2 * blockIdx.x;
+    m[0] = s0 * inv;
+    m[1] = s1 * inv;
+  }
+}
+
+// dgamma and dbeta: the partial sums [parts][2][channels] added in order.
+// kGammaFirst: the first of the two is dgamma's.
+__global__ void __launch_bounds__(kThreads) rf_norm_params_kernel(const float* __restrict__ ws, long long parts,
+                                                                  long long ch, int gamma_first, int pdt,
+                                                                  void* dgamma, void* dbeta) {
+  // 32 channels per block, 8 lanes of parts, merged in order
+  __shared__ float red[2][8][32];
+  const int cl = threadIdx.x & 31, pl = threadIdx.x >> 5;
+  const long long c = (long long)blockIdx.x * 32 + cl;
+  float s0 = 0.f, s1 = 0.f;
+  if (c < ch)
+    for (long long p = pl; p < parts; p += 8) {
+      s0 += ws[p * 2 * ch + c];
+      s1 += ws[p * 2 * ch + ch + c];
+    }
+  red[0][pl][cl] = s0;
+  red[1][pl][cl] = s1;
+  __syncthreads();
+  if (pl == 0 && c < ch) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      s0 += red[0][i][cl];
+      s1 += red[1][i][cl];
+    }
+    store_p(dgamma, pdt, c, gamma_first ? s0 : s1);
+    store_p(dbeta, pdt, c, gamma_first ? s1 : s0);
+  }
+}
+
+// y (or dx) of every element from the statistics.
+template <class T, int VEC, bool kBwd>
+__global__ void __launch_bounds__(kThreads) rf_norm_apply_kernel(const __grid_constant__ NormArgs a, int tile) {
+  const int b = blockIdx.z;
+  const long long ch = (long long)a.groups * a.width;
+  const int lanes = kThreads / tile, rl = threadIdx.x / tile;
+  const long long c = ((long long)blockIdx.y * tile + threadIdx.x % tile) * VEC;
+  if (rl >= lanes || c >= ch) return;
+  float gm[VEC], bt[VEC], mu[VEC], rs[VEC], m1[kBwd ? VEC : 1], m2[kBwd ? VEC : 1];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) {
+    const long long at = 2 * (b * (long long)a.groups + (c + k) / a.width);
+    gm[k] = load_p(a.gamma, a.pdt, c + k);
+    bt[k] = load_p(a.beta, a.pdt, c + k);
+    mu[k] = a.stats[at];
+    rs[k] = a.stats[at + 1];
+    if constexpr (kBwd) {
+      const float* m = a.ws + (long long)a.batch * a.slices * 2 * ch + at;
+      m1[k] = m[0];
+      m2[k] = m[1];
+    }
+  }
+  const long long xo = b * a.xs_b + chan_off(c, a.width, a.xs_g), yo = b * a.ys_b + chan_off(c, a.width, a.ys_g);
+  const T* x = static_cast<const T*>(a.x) + xo;
+  const T* dy = static_cast<const T*>(a.dy) + (kBwd ? yo : 0);
+  T* out = static_cast<T*>(a.y) + (kBwd ? xo : yo);
+  const long long os = kBwd ? a.xs_r : a.ys_r;
+  const long long step = (long long)gridDim.x * lanes;
+#pragma unroll 2
+  for (long long r = (long long)blockIdx.x * lanes + rl; r < a.rows; r += step) {
+    float xv[VEC];
+    load_v<T, VEC>(x + r * a.xs_r, xv);
+    if constexpr (!kBwd) {
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) xv[k] = act_f(fmaf((xv[k] - mu[k]) * rs[k], gm[k], bt[k]), a.act);
+    } else {
+      float dv[VEC];
+      load_v<T, VEC>(dy + r * a.ys_r, dv);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const float xh = (xv[k] - mu[k]) * rs[k];
+        const float gz = dv[k] * act_d(fmaf(xh, gm[k], bt[k]), a.act);
+        xv[k] = rs[k] * (gz * gm[k] - m1[k] - xh * m2[k]);
+      }
+    }
+    store_v<T, VEC>(out + r * os, xv);
+  }
+}
+
+// ---- host -----------------------------------------------------------------------
+
+rf_status_t check_desc(const rf_norm_desc_t* d) {
+  if (!d) return rf_fail(RF_ERR_INVALID_ARG, "null descriptor");
+  if (d->batch < 0 || d->rows < 0) return rf_fail(RF_ERR_INVALID_ARG, "negative batch or rows");
+  if (d->groups < 1 || d->width < 1) return rf_fail(RF_ERR_INVALID_ARG, "groups and width must be > 0");
+  if (d->dtype != RF_BF16 && d->dtype != RF_FP16 && d->dtype != RF_FP32)
+    return rf_fail(RF_ERR_INVALID_ARG, "dtype must be bf16, fp16 or fp32");
+  if (d->param_dtype != RF_BF16 && d->param_dtype != RF_FP16 && d->param_dtype != RF_FP32)
+    return rf_fail(RF_ERR_INVALID_ARG, "param_dtype must be bf16, fp16 or fp32");
+  if (d->span != RF_NORM_ROW && d->span != RF_NORM_SAMPLE) return rf_fail(RF_ERR_INVALID_ARG, "unknown span");
+  if (d->act != RF_ACT_NONE && d->act != RF_ACT_SILU) return rf_fail(RF_ERR_INVALID_ARG, "unknown activation");
+  if (!(d->eps >= 0.f) || !(d->eps < INFINITY)) return rf_fail(RF_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (d->span == RF_NORM_ROW && d->width > kMaxRowWidth)
+    return rf_fail(RF_ERR_UNSUPPORTED, "groups of more than 1024 channels per row are not built");
+  if (d->batch > 65535 && d->span == RF_NORM_SAMPLE)
+    return rf_fail(RF_ERR_UNSUPPORTED, "more than 65535 samples");
+  if (d->groups > 65535) return rf_fail(RF_ERR_UNSUPPORTED, "more than 65535 groups");
+  const int64_t st[] = {d->x_stride_b, d->x_stride_r, d->x_stride_g, d->y_stride_b, d->y_stride_r, d->y_stride_g};
+  for (int64_t s : st)
+    if (s < 0) return rf_fail(RF_ERR_INVALID_ARG, "negative stride");
+  return RF_OK;
+}
+
+int vec_of(const rf_norm_desc_t* d) { return d->dtype == RF_FP32 ? 4 : 8; }
+
+// Channels per thread: 16-byte vectors where every row and group begins on one.
+// Samples may have groups that are no whole number of vectors as long as the
+// channel axis is contiguous.
+bool vector_ok(const rf_norm_desc_t* d, bool rows, const void* a, const void* b, const void* c) {
+  const int v = vec_of(d);
+  if (d->batch > 1 && (d->x_stride_b % v || d->y_stride_b % v)) return false;
+  if (d->rows > 1 && (d->x_stride_r % v || d->y_stride_r % v)) return false;
+  const bool split = d->width % v == 0 && d->x_stride_g % v == 0 && d->y_stride_g % v == 0;
+  const bool whole = !rows && d->x_stride_g == d->width && d->y_stride_g == d->width &&
+                     ((int64_t)d->groups * d->width) % v == 0;
+  if (!split && !whole) return false;
+  const void* ps[] = {a, b, c};
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+  return true;
+}
+
+// Row slices.  Rows: about six CTAs per SM over all groups, at least a few rows
+// per sub-warp; samples: about four CTAs per SM, at least 32 rows each.
+int slices_of(const rf_norm_desc_t* d) {
+  if (d->span == RF_NORM_ROW) {
+    const int64_t n = d->batch * d->rows;
+    const int64_t want = (148 * 6 + d->groups - 1) / d->groups, most = (n + 31) / 32;
+    return (int)std::max<int64_t>(1, std::min(want, most));
+  }
+  const int64_t b = std::max<int64_t>(1, d->batch);
+  const int64_t tiles = ((int64_t)d->groups * d->width + 2047) / 2048;
+  const int64_t want = (148 * 4 + b * tiles - 1) / (b * tiles), most = (d->rows + 31) / 32;
+  return (int)std::max<int64_t>(1, std::min(want, most));
+}
+
+int64_t ws_bytes_of(const rf_norm_desc_t* d) {
+  const int64_t ch = (int64_t)d->groups * d->width, sl = slices_of(d);
+  const int64_t parts = d->span == RF_NORM_ROW ? sl : d->batch * sl;
+  return (parts * 2 * ch + 2 * d->batch * d->groups) * 4 + 256;
+}
+
+NormArgs make_args(const rf_norm_desc_t* d, const void* x, const void* gamma, const void* beta, const void* dy, void* y,
+                   float* stats, void* ws) {
+  NormArgs a;
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.dy = dy;
+  a.y = y;
+  a.stats = stats;
+  a.ws = static_cast<float*>(ws);
+  a.rows = d->rows;
+  a.n_rows = d->batch * d->rows;
+  a.xs_b = d->x_stride_b; a.xs_r = d->x_stride_r; a.xs_g = d->x_stride_g;
+  a.ys_b = d->y_stride_b; a.ys_r = d->y_stride_r; a.ys_g = d->y_stride_g;
+  a.batch = (int)d->batch;
+  a.groups = d->groups;
+  a.width = d->width;
+  a.pdt = d->param_dtype;
+  a.act = d->act;
+  a.slices = slices_of(d);
+  a.eps = d->eps;
+  return a;
+}
+
+template <class T, int VEC, int NV, bool kBwd>
+void row_launch(const NormArgs& a, int lanes, cudaStream_t st) {
+  rf_norm_row_kernel<T, VEC, NV, kBwd><<<dim3((unsigned)a.slices, (unsigned)a.groups), kThreads, 0, st>>>(a, lanes);
+}
+
+template <class T, bool kBwd>
+rf_status_t run_rows(const NormArgs& a, bool vec, cudaStream_t st) {
+  constexpr int V = sizeof(T) == 4 ? 4 : 8;
+  const int units = vec ? a.width / V : a.width;
+  int lanes = 1;
+  while (lanes < 32 && lanes < units) lanes <<= 1;
+  const int nv = (units + lanes - 1) / lanes;
+  if (vec) {
+    if (nv <= 1)      row_launch<T, V, 1, kBwd>(a, lanes, st);
+    else if (nv <= 2) row_launch<T, V, 2, kBwd>(a, lanes, st);
+    else              row_launch<T, V, 8, kBwd>(a, lanes, st);
+  } else {
+    if (nv <= 1)      row_launch<T, 1, 1, kBwd>(a, lanes, st);
+    else if (nv <= 4) row_launch<T, 1, 4, kBwd>(a, lanes, st);
+    else              row_launch<T, 1, 32, kBwd>(a, lanes, st);
+  }
+  return rf_check_launch("rf_norm_row_kernel");
+}
+
+// Channel vectors of a block: all of them up to 256, so that a row is read in
+// one piece; the rest of the threads take further rows.
+int tile_of(const NormArgs& a, int vec) {
+  const long long cv = ((long long)a.groups * a.width + vec - 1) / vec;
+  return (int)std::min<long long>(cv, kThreads);
+}
+
+template <class T, int VEC, bool kBwd>
+rf_status_t run_samples_v(const NormArgs& a, cudaStream_t st) {
+  const int tile = tile_of(a, VEC);
+  const long long cv = ((long long)a.groups * a.width + VEC - 1) / VEC;
+  const unsigned tiles = (unsigned)((cv + tile - 1) / tile);
+  if (tiles > 65535u) return rf_fail(RF_ERR_UNSUPPORTED, "too many channels");
+  rf_norm_partial_kernel<T, VEC, kBwd><<<dim3((unsigned)a.slices, tiles, (unsigned)a.batch), kThreads, 0, st>>>(a, tile);
+  rf_status_t s = rf_check_launch("rf_norm_partial_kernel");
+  if (s != RF_OK) return s;
+  if (kBwd) rf_norm_means_kernel<<<(unsigned)(a.batch * a.groups), kThreads, 0, st>>>(a);
+  else      rf_norm_stats_kernel<<<(unsigned)(a.batch * a.groups), kThreads, 0, st>>>(a);
+  if ((s = rf_check_launch("rf_norm_stats_kernel")) != RF_OK) return s;
+  const long long lanes = kThreads / tile;
+  const long long most = (a.rows + lanes - 1) / lanes, want = (148ll * 8 + tiles * a.batch - 1) / (tiles * a.batch);
+  const unsigned gx = (unsigned)std::max<long long>(1, std::min(most, want));
+  rf_norm_apply_kernel<T, VEC, kBwd><<<dim3(gx, tiles, (unsigned)a.batch), kThreads, 0, st>>>(a, tile);
+  return rf_check_launch("rf_norm_apply_kernel");
+}
+
+template <class T, bool kBwd>
+rf_status_t run_t(const rf_norm_desc_t* d, const NormArgs& a, cudaStream_t st) {
+  constexpr int V = sizeof(T) == 4 ? 4 : 8;
+  const bool rows = d->span == RF_NORM_ROW;
+  const bool vec = vector_ok(d, rows, a.x, a.y, kBwd ? a.dy : a.x);
+  if (rows) return run_rows<T, kBwd>(a, vec, st);
+  return vec ? run_samples_v<T, V, kBwd>(a, st) : run_samples_v<T, 1, kBwd>(a, st);
+}
+
+template <bool kBwd>
+rf_status_t run(const rf_norm_desc_t* d, const NormArgs& a, cudaStream_t st) {
+  if (d->dtype == RF_FP32) return run_t<float, kBwd>(d, a, st);
+  if (d->dtype == RF_BF16) return run_t<__nv_bfloat16, kBwd>(d, a, st);
+  return run_t<__half, kBwd>(d, a, st);
+}
+
+rf_status_t check_norm_ws(const rf_norm_desc_t* d, const void* ws, size_t bytes) {
+  if (!ws) return rf_fail(RF_ERR_INVALID_ARG, "null workspace");
+  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0)
+    return rf_fail(RF_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if ((uint64_t)bytes < (uint64_t)ws_bytes_of(d))
+    return rf_fail(RF_ERR_WORKSPACE_TOO_SMALL, "workspace needs " + std::to_string(ws_bytes_of(d)) + " bytes");
+  return RF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+rf_status_t rf_group_norm_workspace_bytes(const rf_norm_desc_t* d, int64_t* out) {
+  rf_clear_error();
+  rf_status_t st = check_desc(d);
+  if (st != RF_OK) return st;
+  if (!out) return rf_fail(RF_ERR_INVALID_ARG, "null out");
+  *out = ws_bytes_of(d);
+  return RF_OK;
+}
+
+rf_status_t rf_group_norm(const rf_norm_desc_t* d, const void* x, const void* gamma, const void* beta, void* y,
+                          float* stats, void* ws, size_t ws_bytes, rf_stream_t stream) {
+  rf_clear_error();
+  rf_status_t st = check_desc(d);
+  if (st != RF_OK) return st;
+  if (!gamma || !beta) return rf_fail(RF_ERR_INVALID_ARG, "null gamma or beta");
+  const bool sample = d->span == RF_NORM_SAMPLE;
+  if (d->batch == 0 || d->rows == 0) return RF_OK;
+  if (!x || !y || (sample && !stats)) return rf_fail(RF_ERR_INVALID_ARG, "null tensor");
+  if (x == y) return rf_fail(RF_ERR_INVALID_ARG, "y aliases x");
+  if (sample && (st = check_norm_ws(d, ws, ws_bytes)) != RF_OK) return st;
+  if ((st = rf_require_device()) != RF_OK) return st;
+  return run<false>(d, make_args(d, x, gamma, beta, nullptr, y, stats, ws), (cudaStream_t)stream);
+}
+
+rf_status_t rf_group_norm_backward(const rf_norm_desc_t* d, const void* x, const void* gamma, const void* beta,
+                                   const void* dy, const float* stats, void* dx, void* dgamma, void* dbeta, void* ws,
+                                   size_t ws_bytes, rf_stream_t stream) {
+  rf_clear_error();
+  rf_status_t st = check_desc(d);
+  if (st != RF_OK) return st;
+  if (!gamma || !beta || !dgamma || !dbeta) return rf_fail(RF_ERR_INVALID_ARG, "null parameter or its gradient");
+  const bool sample = d->span == RF_NORM_SAMPLE;
+  const int64_t ch = (int64_t)d->groups * d->width;
+  if (d->batch == 0 || d->rows == 0) {
+    if ((st = rf_require_device()) != RF_OK) return st;
+    const size_t bytes = (size_t)ch * (d->param_dtype == RF_FP32 ? 4 : 2);
+    if (cudaMemsetAsync(dgamma, 0, bytes, (cudaStream_t)stream) != cudaSuccess ||
+        cudaMemsetAsync(dbeta, 0, bytes, (cudaStream_t)stream) != cudaSuccess)
+      return rf_check_launch("cudaMemsetAsync(group norm gradients)");
+    return RF_OK;
+  }
+  if (!x || !dy || !dx || (sample && !stats)) return rf_fail(RF_ERR_INVALID_ARG, "null tensor");
+  if (dx == x || dx == dy) return rf_fail(RF_ERR_INVALID_ARG, "dx aliases an input");
+  if ((st = check_norm_ws(d, ws, ws_bytes)) != RF_OK) return st;
+  if ((st = rf_require_device()) != RF_OK) return st;
+  const NormArgs a = make_args(d, x, gamma, beta, dy, dx, const_cast<float*>(stats), ws);
+  if ((st = run<true>(d, a, (cudaStream_t)stream)) != RF_OK) return st;
+  rf_norm_params_kernel<<<(unsigned)((ch + 31) / 32), kThreads, 0, (cudaStream_t)stream>>>(
+      a.ws, sample ? (long long)a.batch * a.slices : (long long)a.slices, ch, sample ? 0 : 1, a.pdt, dgamma, dbeta);
+  return rf_check_launch("rf_norm_params_kernel");
+}
+
+}  // extern "C"

@@ -29,7 +29,7 @@
 
 namespace {
 
-enum Mode { kRearrange = 0, kInverse = 1, kPoolOnly = 2, kQuantOnly = 3 };
+enum Mode { kRearrange = 0, kInverse = 1, kPoolOnly = 2, kQuantOnly = 3, kGather = 4 };
 enum Quant { kQuantNone = 0, kQuantE4M3 = 1, kQuantMx = 2, kQuantFp8 = 3 };
 
 // Outputs of the fused quantization.  Precision "mix": one-byte E4M3 copies of
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads)
   // 16-byte chunk): the permutation's divisions stay off the copy loop.
   if (threadIdx.x < nrows) {
     const int r = r0 + (int)threadIdx.x;
-    const int from = (MODE == kRearrange) ? rf_orig_row(s, r) : r;
+    const int from = (MODE == kRearrange || MODE == kGather) ? rf_orig_row(s, r) : r;
     const int to = (MODE == kInverse) ? rf_orig_row(s, r) : r;
     src_off[threadIdx.x] = (long long)(rf_row_offset(g, s, heads, head, from) / 8);
     dst_off[threadIdx.x] = (long long)(rf_row_offset(g, s, heads, head, to) / 8);
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads)
     val[i] = make_uint4(0, 0, 0, 0);
     if (rr < nrows) val[i] = __ldg(src + src_off[rr] + ch);
   }
-  if (MODE == kRearrange || MODE == kInverse) {
+  if (MODE == kRearrange || MODE == kInverse || MODE == kGather) {
 #pragma unroll
     for (int i = 0; i < kRowsPerThread; ++i) {
       const int rr = rl + i * kRowLanes;
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads)
       if (threadIdx.x == 0) qo.v_exp[(size_t)head * g.t_qblk + tb] = e;
     }
   }
-  if constexpr (MODE == kInverse || MODE == kQuantOnly) {
+  if constexpr (MODE == kInverse || MODE == kQuantOnly || MODE == kGather) {
     return;
   } else {
     if (!pool) return;  // uniform over the CTA
@@ -432,8 +432,9 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int MODE>
 rf_status_t launch(const rf_plan* p, const void* q, const void* k, const void* v, void* qo,
-                   void* ko, void* vo, void* ws, cudaStream_t st, int tensor_heads) {
-  const RfGeomDev& g = p->g;
+                   void* ko, void* vo, void* ws, cudaStream_t st, int tensor_heads, int first_heads = 0) {
+  RfGeomDev g = p->g;
+  if (first_heads) g.n1 = first_heads;  // one tensor of that many heads
   const long long grid = (long long)g.t_qblk * tensor_heads;
   if (grid == 0) return RF_OK;
   if (grid > 0x7FFFFFFFll) return rf_fail(RF_ERR_INVALID_ARG, "grid too large");
@@ -519,4 +520,10 @@ rf_status_t rf_launch_quantize(const rf_plan* p, const void* q_r, const void* k_
 
 rf_status_t rf_launch_inverse(const rf_plan* p, const void* o_r, void* o, cudaStream_t st) {
   return launch<kInverse>(p, o_r, nullptr, nullptr, o, nullptr, nullptr, nullptr, st, p->g.n1);
+}
+
+rf_status_t rf_launch_gather(const rf_plan* p, int heads, const void* x, void* x_r, bool inverse,
+                             cudaStream_t st) {
+  return inverse ? launch<kInverse>(p, x, nullptr, nullptr, x_r, nullptr, nullptr, nullptr, st, heads, heads)
+                 : launch<kGather>(p, x, nullptr, nullptr, x_r, nullptr, nullptr, nullptr, st, heads, heads);
 }

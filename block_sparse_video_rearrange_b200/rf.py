@@ -31,12 +31,17 @@ ORDERS = {"tile": 0, "frame_pair": 1}   # rf_token_order_t
 PRECISIONS = {"native": 0, "mix": 1, "fp8": 2, "mxfp4": 3}   # rf_precision_t
 TORCH_DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
 POOL_MODES = {"from_ws": 0, "recompute": 1}
+DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # rf_dtype_t
+SPANS = {"row": 0, "sample": 1}   # rf_norm_span_t
+ACTS = {"none": 0, "silu": 1}     # rf_act_t
 
 EXPORTED = ("rf_plan_create", "rf_plan_info", "rf_plan_seq_info", "rf_rearrange", "rf_pool_select",
             "rf_block_sparse_attn", "rf_inverse_rearrange", "rf_forward", "rf_check_device_status",
             "rf_plan_destroy", "rf_status_string", "rf_last_error", "rf_plan_permutation",
             "rf_selftest_exp2", "rf_pool_select_noalloc", "rf_plan_create_ex", "rf_quantize_qk",
-            "rf_selftest_expired_wait", "rf_quantize_mx", "rf_quantize")
+            "rf_selftest_expired_wait", "rf_quantize_mx", "rf_quantize", "rf_diff_lambda",
+            "rf_diff_lambda_backward", "rf_diff_attn_workspace_bytes", "rf_diff_attn", "rf_diff_attn_backward",
+            "rf_rearrange_rows", "rf_group_norm_workspace_bytes", "rf_group_norm", "rf_group_norm_backward")
 
 
 class RfError(RuntimeError):
@@ -78,6 +83,14 @@ class SeqInfo(ctypes.Structure):
                 ("k_kv", ctypes.c_int32)]
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("groups", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("x_stride_b", ctypes.c_int64), ("x_stride_r", ctypes.c_int64),
+                ("x_stride_g", ctypes.c_int64), ("y_stride_b", ctypes.c_int64), ("y_stride_r", ctypes.c_int64),
+                ("y_stride_g", ctypes.c_int64), ("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("span", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m block_sparse_video_rearrange_b200.build`")
@@ -104,6 +117,15 @@ def _load() -> ctypes.CDLL:
         "rf_selftest_exp2": [vp, vp, vp, ctypes.c_int64, vp],
         "rf_pool_select_noalloc": [vp, vp, vp, vp, vp, vp],
         "rf_plan_permutation": [vp, i32, ctypes.POINTER(ctypes.c_int64), ctypes.c_int64],
+        "rf_diff_lambda": [vp, vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, vp],
+        "rf_diff_lambda_backward": [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp],
+        "rf_diff_attn_workspace_bytes": [vp, i32, ctypes.POINTER(ctypes.c_int64)],
+        "rf_diff_attn": [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, sz, vp],
+        "rf_diff_attn_backward": [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "rf_rearrange_rows": [vp, i32, vp, vp, i32, vp],
+        "rf_group_norm_workspace_bytes": [ctypes.POINTER(NormDesc), ctypes.POINTER(ctypes.c_int64)],
+        "rf_group_norm": [ctypes.POINTER(NormDesc), vp, vp, vp, vp, vp, vp, sz, vp],
+        "rf_group_norm_backward": [ctypes.POINTER(NormDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "rf_status_string": [i32],
         "rf_last_error": [],
     }
@@ -379,6 +401,221 @@ def forward(plan: Plan, q, k, v, bufs: Buffers, scale: Optional[float] = None, s
                            _ptr(b.select_idx), _ptr(b.select_num), float(scale), _ptr(b.o_r), _ptr(b.o),
                            _ptr(b.ws), b.ws.numel() * b.ws.element_size(), _stream(stream)), "rf_forward")
     return b.o
+
+
+# ---- differential attention and the group norm -----------------------------------------
+
+def _device_of(*tensors) -> int:
+    """The CUDA device all of the tensors (None allowed) live on."""
+    dev = -1
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("librf takes CUDA tensors")
+        d = t.get_device()
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"tensors on different devices: cuda:{dev} and cuda:{d}")
+    return dev
+
+
+def _call(where: str, dev: int, stream, *args) -> None:
+    """Run a librf entry point with `dev` current, on `stream` or the device's current stream."""
+    fn = getattr(_lib, where)
+    if torch.cuda.current_device() == dev:
+        st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+        _check(fn(*args, st), where)
+    else:
+        with torch.cuda.device(dev):
+            st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+            _check(fn(*args, st), where)
+
+
+def _bytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _lambda_vectors(vecs, outs=()) -> Tuple[int, int, int]:
+    a = vecs[0]
+    if a.dim() != 2 or a.dtype not in DTYPE_CODES:
+        raise ValueError(f"lambda's vectors: expected [heads or 1, dim] in bf16, fp16 or fp32, got {tuple(a.shape)} {a.dtype}")
+    for t in (*vecs[1:], *outs):
+        _expect(t, a.shape, a.dtype, "lambda's vectors")
+    return DTYPE_CODES[a.dtype], a.shape[0], a.shape[1]
+
+
+def diff_lambda(a, b, c, d, lambda_init: float, lam, stream=None) -> None:
+    """lam[n] = exp(a[n] . b[n]) - exp(c[n] . d[n]) + lambda_init, fp32 [heads]; the vectors are
+    [heads, dim], or [1, dim] shared by every head."""
+    dt, rows, dim = _lambda_vectors((a, b, c, d))
+    _expect(lam, (lam.numel(),), torch.float32, "lam")
+    _call("rf_diff_lambda", _device_of(a, b, c, d, lam), stream, _ptr(a), _ptr(b), _ptr(c), _ptr(d), dt, rows, dim,
+          lam.numel(), float(lambda_init), _ptr(lam))
+
+
+def diff_lambda_backward(a, b, c, d, dlam, da, db, dc, dd, stream=None) -> None:
+    """Gradients of lambda's vectors from dlam (fp32 [heads])."""
+    dt, rows, dim = _lambda_vectors((a, b, c, d), (da, db, dc, dd))
+    _expect(dlam, (dlam.numel(),), torch.float32, "dlam")
+    _call("rf_diff_lambda_backward", _device_of(a, b, c, d, dlam, da, db, dc, dd), stream, _ptr(a), _ptr(b), _ptr(c),
+          _ptr(d), dt, rows, dim, dlam.numel(), _ptr(dlam), _ptr(da), _ptr(db), _ptr(dc), _ptr(dd))
+
+
+def diff_attn_workspace_bytes(plan: Plan, backward: bool = False) -> int:
+    """Device workspace of diff_attn (and diff_attn_backward); it holds the plan's own too."""
+    out = ctypes.c_int64()
+    _check(_lib.rf_diff_attn_workspace_bytes(plan.handle, int(backward), ctypes.byref(out)),
+           "rf_diff_attn_workspace_bytes")
+    return out.value
+
+
+def _expect_attn(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, maps, lse) -> None:
+    for t, h, nm in ((q_r, plan.n1, "q_r"), (k_r, plan.n2, "k_r"), (v_r, plan.n2, "v_r")):
+        _expect(t, plan.tensor_shape(h), plan.torch_dtype, nm)
+    si, sn = plan.select_shapes()
+    _expect(select_idx, si, torch.int32, "select_idx")
+    _expect(select_num, sn, torch.int32, "select_num")
+    _expect(lam, (plan.n1,), torch.float32, "lam")
+    if maps is not None:
+        _expect(maps, (2, *plan.tensor_shape(plan.n1)), torch.float32, "maps")
+    if lse is not None:
+        _expect(lse, (2, plan.n1, int(plan.info.rows_total)), torch.float32, "lse")
+
+
+def diff_attn(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, scale: float, o_r, ws, maps=None, lse=None,
+              stream=None) -> None:
+    """(softmax(scale Q_1 K_1^T) - lam softmax(scale Q_2 K_2^T)) V over the selected blocks, the maps'
+    Q and K being the two halves of each head's columns (rearranged order).  maps and lse (both or
+    neither) receive what diff_attn_backward needs."""
+    _expect_attn(plan, q_r, k_r, v_r, select_idx, select_num, lam, maps, lse)
+    _expect(o_r, plan.tensor_shape(plan.n1), plan.torch_dtype, "o_r")
+    dev = _device_of(q_r, k_r, v_r, select_idx, select_num, lam, o_r, ws, maps, lse)
+    _call("rf_diff_attn", dev, stream, plan.handle, _ptr(q_r), _ptr(k_r), _ptr(v_r), _ptr(select_idx), _ptr(select_num),
+          _ptr(lam), float(scale), _ptr(o_r), _ptr(maps), _ptr(lse), _ptr(ws), _bytes(ws))
+
+
+def diff_attn_backward(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, scale: float, maps, lse, do_r, dq_r, dk_r,
+                       dv_r, dlam, ws, stream=None) -> None:
+    """Gradients of diff_attn from do_r and what it kept (maps, lse); rearranged order."""
+    _expect_attn(plan, q_r, k_r, v_r, select_idx, select_num, lam, maps, lse)
+    for t, h, nm in ((do_r, plan.n1, "do_r"), (dq_r, plan.n1, "dq_r"), (dk_r, plan.n2, "dk_r"), (dv_r, plan.n2, "dv_r")):
+        _expect(t, plan.tensor_shape(h), plan.torch_dtype, nm)
+    _expect(dlam, (plan.n1,), torch.float32, "dlam")
+    dev = _device_of(q_r, k_r, v_r, select_idx, select_num, lam, maps, lse, do_r, dq_r, dk_r, dv_r, dlam, ws)
+    _call("rf_diff_attn_backward", dev, stream, plan.handle, _ptr(q_r), _ptr(k_r), _ptr(v_r), _ptr(select_idx),
+          _ptr(select_num), _ptr(lam), float(scale), _ptr(maps), _ptr(lse), _ptr(do_r), _ptr(dq_r), _ptr(dk_r), _ptr(dv_r),
+          _ptr(dlam), _ptr(ws), _bytes(ws))
+
+
+def rearrange_rows(plan: Plan, x, y, inverse: bool = False, stream=None) -> None:
+    """The plan's row permutation of one tensor (of n1 or n2 heads), or its inverse."""
+    heads = x.shape[1]
+    _expect(x, plan.tensor_shape(heads), plan.torch_dtype, "x")
+    _expect(y, plan.tensor_shape(heads), plan.torch_dtype, "y")
+    _call("rf_rearrange_rows", _device_of(x, y), stream, plan.handle, heads, _ptr(x), _ptr(y), int(inverse))
+
+
+class DiffBuffers:
+    """Device buffers of differential attention on one plan (owned by torch)."""
+
+    def __init__(self, plan: Plan, train: bool = False, device="cuda"):
+        shp_q, shp_kv, dt = plan.tensor_shape(plan.n1), plan.tensor_shape(plan.n2), plan.torch_dtype
+        f32 = dict(dtype=torch.float32, device=device)
+        self.o_r = torch.empty(shp_q, dtype=dt, device=device)
+        self.lam = torch.empty(plan.n1, **f32)
+        self.ws = torch.zeros(diff_attn_workspace_bytes(plan, train) // 4 + 64, dtype=torch.int32, device=device)
+        self.maps = self.lse = None
+        if train:
+            self.maps = torch.empty((2, *shp_q), **f32)
+            self.lse = torch.empty((2, plan.n1, int(plan.info.rows_total)), **f32)
+            self.dq_r = torch.empty(shp_q, dtype=dt, device=device)
+            self.dk_r = torch.empty(shp_kv, dtype=dt, device=device)
+            self.dv_r = torch.empty(shp_kv, dtype=dt, device=device)
+            self.dlam = torch.empty(plan.n1, **f32)
+
+
+def _norm_strides(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    if t.dim() != 4:
+        raise ValueError(f"{name}: expected [batch, rows, groups, width], got {tuple(t.shape)}")
+    sb, sr, sg, sc = t.stride()
+    if sc != 1 and t.shape[3] > 1 and t.numel():
+        raise ValueError(f"{name}: the channels of a group must be contiguous")
+    return sb, sr, sg
+
+
+def _norm_desc(x, span: str, act: str, eps: float, param_dtype=torch.float32, y=None) -> NormDesc:
+    if span not in SPANS:
+        raise ValueError(f"span must be one of {sorted(SPANS)}")
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}")
+    if x.dtype not in DTYPE_CODES or param_dtype not in DTYPE_CODES:
+        raise ValueError(f"group norm takes bf16, fp16 or fp32, got {x.dtype} and {param_dtype}")
+    xs = _norm_strides(x, "x")
+    ys = xs if y is None else _norm_strides(y, "y")
+    return NormDesc(x.shape[0], x.shape[1], x.shape[2], x.shape[3], *xs, *ys, DTYPE_CODES[x.dtype],
+                    DTYPE_CODES[param_dtype], SPANS[span], ACTS[act], float(eps))
+
+
+def group_norm_workspace(x, span: str = "row") -> torch.Tensor:
+    """A device workspace for group_norm and group_norm_backward of tensors like x."""
+    out = ctypes.c_int64()
+    _check(_lib.rf_group_norm_workspace_bytes(ctypes.byref(_norm_desc(x, span, "none", 0.0)), ctypes.byref(out)),
+           "rf_group_norm_workspace_bytes")
+    return torch.empty(out.value // 4 + 64, dtype=torch.int32, device=x.device)
+
+
+def group_norm_stats(x, span: str = "row") -> Optional[torch.Tensor]:
+    """What group_norm keeps for its backward pass: fp32 [batch, groups, 2] with span "sample", None with "row"."""
+    return torch.empty((x.shape[0], x.shape[2], 2), dtype=torch.float32, device=x.device) if span == "sample" else None
+
+
+def _norm_params(x, *params) -> torch.dtype:
+    pdt = params[0].dtype
+    for t in params:
+        _expect(t, (x.shape[2], x.shape[3]), pdt, "gamma, beta and their gradients")
+    return pdt
+
+
+def group_norm(x, gamma, beta, y, span: str = "row", act: str = "none", eps: float = 1e-5, stats=None, ws=None,
+               stream=None) -> None:
+    """y = act(gamma (x - mu) / sqrt(var + eps) + beta) of x [batch, rows, groups, width], mu and var over a group's
+    channels of each row (span "row") or of all rows of a batch element ("sample").  gamma, beta: [groups, width].
+    Span "sample" takes ws (group_norm_workspace) and keeps stats (group_norm_stats) for the backward pass."""
+    _expect(y, x.shape, x.dtype, "y")
+    desc = _norm_desc(x, span, act, eps, _norm_params(x, gamma, beta), y)
+    if span == "sample":
+        if ws is None:
+            ws = group_norm_workspace(x, span)
+        if stats is None:
+            stats = group_norm_stats(x, span)
+        _expect(stats, (x.shape[0], x.shape[2], 2), torch.float32, "stats")
+    else:
+        stats = None
+    _call("rf_group_norm", _device_of(x, gamma, beta, y, stats, ws), stream, ctypes.byref(desc), x.data_ptr(), _ptr(gamma),
+          _ptr(beta), y.data_ptr(), _ptr(stats), _ptr(ws), _bytes(ws))
+
+
+def group_norm_backward(x, gamma, beta, dy, stats, dx, dgamma, dbeta, span: str = "row", act: str = "none",
+                        eps: float = 1e-5, ws=None, stream=None) -> None:
+    """Gradients of group_norm; stats as it kept them (None with span "row")."""
+    _expect(dy, x.shape, x.dtype, "dy")
+    _expect(dx, x.shape, x.dtype, "dx")
+    desc = _norm_desc(x, span, act, eps, _norm_params(x, gamma, beta, dgamma, dbeta), dy)
+    if _norm_strides(dx, "dx") != _norm_strides(x, "x"):
+        raise ValueError("dx must have x's strides")
+    if span == "sample":
+        if stats is None:
+            raise ValueError("span sample needs the stats that group_norm kept")
+        _expect(stats, (x.shape[0], x.shape[2], 2), torch.float32, "stats")
+    else:
+        stats = None
+    if ws is None:
+        ws = group_norm_workspace(x, span)
+    _call("rf_group_norm_backward", _device_of(x, gamma, beta, dy, stats, dx, dgamma, dbeta, ws), stream,
+          ctypes.byref(desc), x.data_ptr(), _ptr(gamma), _ptr(beta), dy.data_ptr(), _ptr(stats), dx.data_ptr(),
+          _ptr(dgamma), _ptr(dbeta), _ptr(ws), _bytes(ws))
 
 
 _PIPELINES = {}        # host pipelines (with their device buffers) of recent problem shapes

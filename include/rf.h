@@ -85,7 +85,9 @@ typedef enum {
 } rf_status_t;
 
 typedef enum { RF_LAYOUT_BNSD = 0, RF_LAYOUT_TND = 1 } rf_layout_t;
-typedef enum { RF_BF16 = 0, RF_FP16 = 1 } rf_dtype_t;
+/* Plans take bf16 and fp16; RF_FP32 is for the parameters of lambda and the
+ * tensors and parameters of the group norm. */
+typedef enum { RF_BF16 = 0, RF_FP16 = 1, RF_FP32 = 2 } rf_dtype_t;
 
 /* How rf_pool_select obtains the block means of Q and K. */
 typedef enum {
@@ -415,6 +417,111 @@ RF_API rf_status_t rf_forward(const rf_plan_t* plan, const void* q, const void* 
  * r < length.  n must equal rf_seq_info_t.length.  This is the same index
  * arithmetic the kernels run ([UG] "Geometry handling"). */
 RF_API rf_status_t rf_plan_permutation(const rf_plan_t* plan, int32_t seq, int64_t* src_rows, int64_t n);
+
+/* ---- Differential attention ------------------------------------------------
+ * The difference of two softmax maps with learned weights, over the same
+ * selection as rf_block_sparse_attn.  With Q_1, Q_2 the first and second half
+ * of a query head's d columns and K_1, K_2 those of its key head,
+ *     P_w = softmax(scale * Q_w K_w^T)   over the rows of the listed key blocks
+ *     O   = (P_1 - lambda_n P_2) V       lambda_n one number per query head n.
+ * Shapes, layouts, rearrangement, selection (the ranking's q . k is the sum of
+ * both maps' scores) and the inverse are those of a plan with the same heads;
+ * scale is typically 1 / sqrt(d / 2).  Native precision and blockShape 128 x 128
+ * (RF_ERR_UNSUPPORTED otherwise). */
+
+/* lambda[n] = exp(a[n] . b[n]) - exp(c[n] . d[n]) + lambda_init.
+ * a, b, c, d  : the learned vectors, contiguous [vec_heads, dim] of dtype (bf16,
+ *               fp16 or fp32); vec_heads is heads, or 1 (shared by every head).
+ * lambda      : fp32 [heads].  dim and heads > 0, lambda_init finite. */
+RF_API rf_status_t rf_diff_lambda(const void* a, const void* b, const void* c, const void* d,
+                                  rf_dtype_t dtype, int32_t vec_heads, int32_t dim, int32_t heads,
+                                  float lambda_init, float* lambda, rf_stream_t stream);
+/* Gradients of the vectors (their shape and dtype) from dlambda, fp32 [heads];
+ * vectors shared by every head get the sum over the heads.  Deterministic. */
+RF_API rf_status_t rf_diff_lambda_backward(const void* a, const void* b, const void* c,
+                                           const void* d, rf_dtype_t dtype, int32_t vec_heads,
+                                           int32_t dim, int32_t heads, const float* dlambda,
+                                           void* da, void* db, void* dc, void* dd,
+                                           rf_stream_t stream);
+/* Device workspace of rf_diff_attn (backward == 0) or of both rf_diff_attn and
+ * rf_diff_attn_backward (backward != 0).  It begins with the plan's own workspace
+ * (status words, block means), so one buffer serves every call on the plan; zero
+ * it once.  Calls that may overlap on the GPU need a workspace each.  Host only. */
+RF_API rf_status_t rf_diff_attn_workspace_bytes(const rf_plan_t* plan, int32_t backward,
+                                                int64_t* out);
+/* q_r, k_r, v_r, o_r, select_idx, select_num, scale : as rf_block_sparse_attn,
+ *               16-byte aligned, contiguous, in rearranged order; the entries of a
+ *               selectIdx row are ascending: -1 is an unused slot, and an entry out
+ *               of range, or not larger than one before it, is skipped and counted
+ *               in the status words.  A row without entries gives O = 0.
+ * lambda      : fp32 [n1].
+ * maps, lse   : both NULL (serving), or both given for the backward pass:
+ *               maps fp32 [2, shape of o_r] receives P_1 V and P_2 V, lse fp32
+ *               [2, n1, rows_total] the log2 of each row's sum of exponentials
+ *               (+infinity for a row without entries).
+ * The difference is taken in fp32 and rounded once; P is held in f16.
+ * Values of K and V rows outside the listed blocks never reach O, whatever they
+ * are.  Deterministic. */
+RF_API rf_status_t rf_diff_attn(const rf_plan_t* plan, const void* q_r, const void* k_r,
+                                const void* v_r, const int32_t* select_idx,
+                                const int32_t* select_num, const float* lambda, float scale,
+                                void* o_r, float* maps, float* lse, void* ws, size_t ws_bytes,
+                                rf_stream_t stream);
+/* Gradients of rf_diff_attn: q_r .. scale as given to it, maps and lse as it
+ * wrote them, do_r the gradient of o_r (its shape and type).
+ * dq_r, dk_r, dv_r : gradients, shapes and types of q_r, k_r, v_r (rows in
+ *               rearranged order; rf_rearrange_rows puts them back), summed over
+ *               the query heads that share a key/value head; rows that nothing
+ *               lists get zeros.  dlambda: fp32 [n1].
+ * Deterministic: no atomic additions, every sum in a fixed order. */
+RF_API rf_status_t rf_diff_attn_backward(const rf_plan_t* plan, const void* q_r, const void* k_r,
+                                         const void* v_r, const int32_t* select_idx,
+                                         const int32_t* select_num, const float* lambda,
+                                         float scale, const float* maps, const float* lse,
+                                         const void* do_r, void* dq_r, void* dk_r, void* dv_r,
+                                         float* dlambda, void* ws, size_t ws_bytes,
+                                         rf_stream_t stream);
+/* The plan's row permutation of one tensor of `heads` heads (n1 or n2): to
+ * rearranged order (inverse == 0), or back (inverse != 0).  The gradient of one
+ * direction is the other. */
+RF_API rf_status_t rf_rearrange_rows(const rf_plan_t* plan, int32_t heads, const void* x, void* y,
+                                     int32_t inverse, rf_stream_t stream);
+
+/* ---- Group norm with an activation -----------------------------------------
+ * x is [batch, rows, groups, width] with any non-negative strides of the first
+ * three axes and contiguous channels of a group: a channels-last feature map
+ * [batch, rows, groups * width], a TND attention output [1, T, heads, d], or a
+ * BNSD one [B, L, heads, d] as a transposed view.
+ *     mu, var : over a group's channels of one row (RF_NORM_ROW), or of all rows
+ *               of a batch element (RF_NORM_SAMPLE)
+ *     y = act(gamma * (x - mu) / sqrt(var + eps) + beta)
+ * gamma, beta: [groups, width] of param_dtype. */
+typedef enum { RF_NORM_ROW = 0, RF_NORM_SAMPLE = 1 } rf_norm_span_t;
+typedef enum { RF_ACT_NONE = 0, RF_ACT_SILU = 1 } rf_act_t;
+typedef struct {
+  int64_t batch, rows;                          /* >= 0 */
+  int32_t groups, width;                        /* > 0; RF_NORM_ROW: width <= 1024 */
+  int64_t x_stride_b, x_stride_r, x_stride_g;   /* of x and dx, in elements */
+  int64_t y_stride_b, y_stride_r, y_stride_g;   /* of y and dy */
+  int32_t dtype, param_dtype;                   /* rf_dtype_t */
+  int32_t span;                                 /* rf_norm_span_t */
+  int32_t act;                                  /* rf_act_t */
+  float eps;                                    /* finite, >= 0 */
+} rf_norm_desc_t;
+/* Workspace of both calls (host only). */
+RF_API rf_status_t rf_group_norm_workspace_bytes(const rf_norm_desc_t* desc, int64_t* out);
+/* stats: RF_NORM_SAMPLE: fp32 [batch, groups, 2], receives {mu, 1 / sqrt(var +
+ * eps)}, which the backward pass reads; RF_NORM_ROW: may be NULL (and so may ws).
+ * Outputs must not overlap inputs. */
+RF_API rf_status_t rf_group_norm(const rf_norm_desc_t* desc, const void* x, const void* gamma,
+                                 const void* beta, void* y, float* stats, void* ws,
+                                 size_t ws_bytes, rf_stream_t stream);
+/* dx with x's strides and type; dgamma, dbeta [groups, width] of param_dtype, summed
+ * over batch and rows in a fixed order (deterministic). */
+RF_API rf_status_t rf_group_norm_backward(const rf_norm_desc_t* desc, const void* x,
+                                          const void* gamma, const void* beta, const void* dy,
+                                          const float* stats, void* dx, void* dgamma, void* dbeta,
+                                          void* ws, size_t ws_bytes, rf_stream_t stream);
 
 /* Reads and clears the device status words in ws.  Synchronises `stream`.
  * [API] constraints: selectIdx entries must be valid block indices or -1, and
