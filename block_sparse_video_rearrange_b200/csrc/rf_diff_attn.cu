@@ -15,7 +15,7 @@
 // value down to 2^-29 of the block's largest, with the rows past a block's end
 // zero (an unselected row's NaN must not meet P = 0).
 //
-// One CTA = one (query block of 128 rows, query head), head-major.  The work
+// One CTA = one (query block of 128 rows, query head).  The work
 // items of a CTA are (key block b, map w) in the order (0,1), (0,2), (1,1), ...
 // so that K_b and V_b are loaded once for both maps; softmax group w of 128
 // threads (thread = query row = TMEM lane) owns map w with its own running
@@ -87,6 +87,7 @@ struct __align__(1024) DiffSmem {
 
 struct DiffArgs {
   RfGeomDev g;
+  RfOrder order;
   const int32_t* sel_idx;
   const int32_t* sel_num;
   const float* lambda;   // [n1]
@@ -151,8 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const RfGeomDev& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = blockIdx.x / g.t_qblk;
-  const int tb = blockIdx.x % g.t_qblk;
+  int n, tb;
+  rf_cta_item(g, a.order, g.n1, blockIdx.x, n, tb);
   const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
   const int nblk = s.n_pb + s.nb;
   const int gk = n / (g.n1 / g.n2);
@@ -625,6 +626,7 @@ rf_status_t rf_launch_diff_attn(const rf_plan* p, const void* q_r, const void* k
   if ((s = rf_check_launch("rf_diff_prep_v_kernel")) != RF_OK) return s;
   DiffArgs a;
   a.g = g;
+  a.order = rf_order(g);
   a.sel_idx = sel_idx;
   a.sel_num = sel_num;
   a.lambda = lambda;

@@ -39,19 +39,21 @@ namespace {
 constexpr int kThreads = 640;      // four compute warpgroups and one of single-warp roles
 constexpr int kCompute = 512;
 constexpr int kMmaWarp = 16;       // TMEM allocation and every tcgen05.mma
-constexpr int kLoadWarp = 17;      // dQ: Q, dO, K; dK/dV: everything
-constexpr int kLoadVWarp = 18;     // dQ: V
+constexpr int kLoadWarp = 17;      // every load
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBoxBytes = RF_BLOCK * 128;
-constexpr uint32_t kHalf = 64 * 128;  // bytes of 64 rows of a box
-constexpr uint32_t kStatBytes = 4 * RF_BLOCK * 4;
+constexpr uint32_t kHalfBox = 64 * 128;  // bytes of a 64-row box
+constexpr int kQStages = 4;              // dQ: 64-row stages of K and V
+constexpr int kKvStages = 3;             // dK/dV: 64-row stages of Q, dO and the rows' numbers
+constexpr uint32_t kStatBytes = 4 * 64 * 4;
 
 struct BwdArgs {
   RfGeomDev g;
+  RfOrder order;
   const int32_t* sel_idx;
   const int32_t* sel_num;
   const float* lambda;       // [n1]
-  const float* stats;        // [n1][t_qblk][4][128]: -lse_1, -lse_2, delta_1, delta_2
+  const float* stats;        // [n1][t_qblk][2][4][64]: -lse_1, -lse_2, delta_1, delta_2 of 64 rows
   const uint32_t* bits;      // [n1][t_qblk][words]
   const uint32_t* amax;      // fp16: largest |dO|, |V|, |lambda| as fp32 bits
   int words;
@@ -82,10 +84,10 @@ struct __align__(1024) DqSmem {
   static constexpr int kTileBytes = RF_BLOCK * D * 2;
   uint8_t q[kTileBytes];
   uint8_t d_o[kTileBytes];
-  uint8_t k[2][kTileBytes];
-  uint8_t v[2][kTileBytes];
+  uint8_t k[kQStages][kTileBytes / 2];
+  uint8_t v[kQStages][kTileBytes / 2];
   uint64_t bar_q, bar_aux;
-  uint64_t bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2];
+  uint64_t bar_full[kQStages], bar_empty[kQStages];
   uint64_t bar_sd_full[2];  // S_1, S_2 and dA of a 64-key half computed
   uint64_t bar_ds_full[2];  // dS_1 and dS_2 of it stored (and all of S, dA read)
   uint64_t bar_dq_done[2];  // dQ += dS K of it complete
@@ -101,33 +103,34 @@ struct __align__(1024) DkvSmem {
   static constexpr int kTileBytes = RF_BLOCK * D * 2;
   uint8_t k[kTileBytes];
   uint8_t v[kTileBytes];
-  uint8_t q[2][kTileBytes];
-  uint8_t d_o[2][kTileBytes];
-  float stats[2][4][RF_BLOCK];
-  float lam[2];
+  uint8_t q[kKvStages][kTileBytes / 2];
+  uint8_t d_o[kKvStages][kTileBytes / 2];
+  uint8_t a[2][RF_BLOCK * 128];  // A^T of a step: 128 keys x 64 queries, K-major, 128-byte swizzle
+  float stats[kKvStages][4][64];
+  float lam[kKvStages];
   uint64_t bar_kv, bar_aux;
-  uint64_t bar_full[2], bar_empty[2];
-  uint64_t bar_s1_full[2];  // by parity: S_1 of the next step is computed one step ahead
-  uint64_t bar_s2_full, bar_da_full;
+  uint64_t bar_full[kKvStages], bar_empty[kKvStages];
+  uint64_t bar_s1_full[2];  // S_1 computed, the rows' numbers there, A's buffer free; by parity, one step ahead
+  uint64_t bar_da_full;     // S_2 and dA computed
+  uint64_t bar_read;        // S_1, S_2 and dA of a step read into registers
   uint64_t bar_ew;          // A, dS_1, dS_2 of a step stored
-  uint64_t bar_x_done;      // A and dS_1 read by their products
-  uint64_t bar_y_done;      // dS_2 too
+  uint64_t bar_y_done;      // and read by their products
   uint64_t bar_final, bar_drain;
   uint32_t tmem_base;
   int abort;
   int n_items;
 };
 
-// Zeroes rows [nrows, 128) of a tile's 128-byte-wide boxes (a row is 128 bytes
-// of each box whatever the swizzle), by one warp.
+// Zeroes rows [nrows, 64) of a 64-row tile's 128-byte-wide boxes (a row is 128
+// bytes of each box whatever the swizzle), by one warp.
 __device__ __forceinline__ void zero_tail(uint8_t* tile, int boxes, int nrows, int lane) {
-  const int per_box = (RF_BLOCK - nrows) * 8;
+  const int per_box = (64 - nrows) * 8;
   for (int x = 0; x < boxes; ++x)
     for (int i = lane; i < per_box; i += 32)
-      *reinterpret_cast<uint4*>(tile + x * kBoxBytes + nrows * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(tile + x * kHalfBox + nrows * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// dS of 32 keys of one map for one query row: P = 2^(s * sl2 + nlse), then
+// dS of 16 keys of one map for one query row: P = 2^(s * sl2 + nlse), then
 // P * (dA * c - dc), rounded to 16 bits and packed.
 template <bool kBf16, bool kFull>
 __device__ __forceinline__ void ds_chunk(const uint32_t* s, const uint32_t* da, int c0, int vr, float sl2,
@@ -137,7 +140,7 @@ __device__ __forceinline__ void ds_chunk(const uint32_t* s, const uint32_t* da, 
   const uint64_t cc = rf_f2(__float_as_uint(c), __float_as_uint(c));
   const uint64_t nd = rf_f2(__float_as_uint(-dc), __float_as_uint(-dc));
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
+  for (int i = 0; i < 16; i += 2) {
     float x0, x1, y0, y1;
     rf_f2_split(rf_fma2(rf_f2(s[i], s[i + 1]), sl, nl), x0, x1);
     const uint64_t p = rf_f2(__float_as_uint(rf_ex2(x0)), __float_as_uint(rf_ex2(x1)));
@@ -197,7 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const RfGeomDev& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = blockIdx.x / g.t_qblk, tb = blockIdx.x % g.t_qblk;
+  int n, tb;
+  rf_cta_item(g, a.order, g.n1, blockIdx.x, n, tb);
   const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
   const int nblk = s.n_pb + s.nb;
   const int gk = n / (g.n1 / g.n2);
@@ -213,11 +217,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(rf_smem_u32(&sm.bar_q), 1);
     mbar_init(rf_smem_u32(&sm.bar_aux), 1);
+    for (int i = 0; i < kQStages; ++i) {
+      mbar_init(rf_smem_u32(&sm.bar_full[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_empty[i]), 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(rf_smem_u32(&sm.bar_k_full[i]), 1);
-      mbar_init(rf_smem_u32(&sm.bar_k_empty[i]), 1);
-      mbar_init(rf_smem_u32(&sm.bar_v_full[i]), 1);
-      mbar_init(rf_smem_u32(&sm.bar_v_empty[i]), 1);
       mbar_init(rf_smem_u32(&sm.bar_sd_full[i]), 1);
       mbar_init(rf_smem_u32(&sm.bar_ds_full[i]), 256);
       mbar_init(rf_smem_u32(&sm.bar_dq_done[i]), 1);
@@ -255,15 +259,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   carry_exponents<D, kBf16>(a.amax, ea, es);
 
   if (warp >= 16) {
-    if ((warp == kLoadWarp || warp == kLoadVWarp) && nv > 0) {
-      // ---------------- TMA producers (lane 0 loads; the warp zeroes a partial block's tail) ----------------
-      const bool is_k = warp == kLoadWarp;
-      uint64_t* full = is_k ? sm.bar_k_full : sm.bar_v_full;
-      uint64_t* empty = is_k ? sm.bar_k_empty : sm.bar_v_empty;
-      uint8_t* tiles = is_k ? &sm.k[0][0] : &sm.v[0][0];
-      const void* map = is_k ? static_cast<const void*>(&tm_k) : static_cast<const void*>(&tm_v);
+    if (warp == kLoadWarp && nv > 0) {
+      // ---------------- loads (lane 0; the warp zeroes a partial block's tail) ----------------
       int c1, c2;
-      if (is_k && lane == 0) {
+      if (lane == 0) {
         coords(g.n1, n, q_r0, c1, c2);
         mbar_arrive_expect_tx(rf_smem_u32(&sm.bar_q), 2 * kTileBytes);
         for (int x = 0; x < kBoxes; ++x) {
@@ -272,46 +271,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       volatile int no_abort = 0;
-      int issued = 0, aux_used = 0;
-      for (int b = 0; b < nv; ++b) {
-        const int st = b & 1;
-        if (b >= 2 && !warp_wait(rf_smem_u32(&empty[st]), ((b >> 1) & 1) ^ 1, abort)) {
-          if (lane == 0) record_timeout(abort, a.status, is_k ? 4 : 5);
+      int issued = 0, tails = 0;
+      for (int t = 0; t < 2 * nv; ++t) {  // 64 rows of a key block each
+        const int st = t % kQStages;
+        if (t >= kQStages && !warp_wait(rf_smem_u32(&sm.bar_empty[st]), ((t / kQStages) & 1) ^ 1, abort)) {
+          if (lane == 0) record_timeout(abort, a.status, 4);
           break;
         }
-        const int blk = sm.list[b];
+        const int blk = sm.list[t >> 1];
         // K rows past the prefix meet dS = 0 in dQ: they must be finite.
-        const bool tail = is_k && blk == s.n_pb - 1 && vr_last < RF_BLOCK;
-        const uint32_t bar = rf_smem_u32(tail ? &sm.bar_aux : &full[st]);
+        const int left = blk == s.n_pb - 1 ? vr_last - 64 * (t & 1) : 64;
+        const bool tail = left < 64;
+        const uint32_t bar = rf_smem_u32(tail ? &sm.bar_aux : &sm.bar_full[st]);
         if (lane == 0) {
           int r0, nr;
           rf_block_span(s, blk, r0, nr);
-          coords(g.n2, gk, r0, c1, c2);
+          coords(g.n2, gk, r0 + 64 * (t & 1), c1, c2);
           mbar_arrive_expect_tx(bar, kTileBytes);
-          for (int x = 0; x < kBoxes; ++x)
-            tma_load_3d(rf_smem_u32(tiles + st * kTileBytes + x * kBoxBytes), map, bar, x * 64, c1, c2);
+          for (int x = 0; x < kBoxes; ++x) {
+            tma_load_3d(rf_smem_u32(sm.v[st] + x * kHalfBox), &tm_v, bar, x * 64, c1, c2);
+            tma_load_3d(rf_smem_u32(sm.k[st] + x * kHalfBox), &tm_k, bar, x * 64, c1, c2);
+          }
         }
         __syncwarp();
-        if (tail) {  // at most one block of a list
-          aux_used = 1;
-          const bool landed = warp_wait(bar, 0, &no_abort);
-          if (landed) zero_tail(tiles + st * kTileBytes, kBoxes, vr_last, lane);
+        if (tail) {  // the halves of at most one block
+          const bool landed = warp_wait(bar, tails & 1, &no_abort);
+          ++tails;
+          if (landed) zero_tail(sm.k[st], kBoxes, max(left, 0), lane);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
             if (!landed) record_timeout(abort, a.status, 4);
-            mbar_arrive(rf_smem_u32(&full[st]));
+            mbar_arrive(rf_smem_u32(&sm.bar_full[st]));
           }
           __syncwarp();
         }
-        issued = b + 1;
+        issued = t + 1;
       }
       if (*abort) {
         // Let this warp's own copies land before the shared memory goes away.
-        if (is_k) warp_wait(rf_smem_u32(&sm.bar_q), 0, &no_abort);
-        for (int b = (issued > 2 ? issued - 2 : 0); b < issued; ++b)
-          warp_wait(rf_smem_u32(&full[b & 1]), (b >> 1) & 1, &no_abort);
-        (void)aux_used;
+        warp_wait(rf_smem_u32(&sm.bar_q), 0, &no_abort);
+        for (int t = (issued > kQStages ? issued - kQStages : 0); t < issued; ++t)
+          warp_wait(rf_smem_u32(&sm.bar_full[t % kQStages]), (t / kQStages) & 1, &no_abort);
       }
     } else if (warp == kMmaWarp && nv > 0) {
       // ---------------- tcgen05.mma issue ----------------
@@ -322,70 +323,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t ddo = umma_desc_sw128(rf_smem_u32(sm.d_o), 16, 1024);
       const uint64_t dk0 = umma_desc_sw128(rf_smem_u32(sm.k[0]), 16, 1024);
       const uint64_t dv0 = umma_desc_sw128(rf_smem_u32(sm.v[0]), 16, 1024);
-      const uint64_t dkn0 = umma_desc_sw128(rf_smem_u32(sm.k[0]), kBoxBytes, 1024);
+      const uint64_t dkn0 = umma_desc_sw128(rf_smem_u32(sm.k[0]), kHalfBox, 1024);
       const int nt = 2 * nv;
       auto issue_da = [&](int t) {  // dA of step t
-        const int b = t >> 1, h = t & 1;
-        const uint64_t dv = dv0 + (uint64_t)(((b & 1) * kTileBytes + h * kHalf) >> 4);
+        const int h = t & 1, st = t % kQStages;
+        const uint64_t dv = dv0 + (uint64_t)(st * (kTileBytes / 2) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + 192 * h + 128, ddo + off, dv + off, id_sd, kk > 0 ? 1u : 0u);
+          const uint32_t in = (kk & 3) * 32, box = kk >> 2;
+          mma_ss(tmem + 192 * h + 128, ddo + ((box * kBoxBytes + in) >> 4), dv + ((box * kHalfBox + in) >> 4), id_sd,
+                 kk > 0 ? 1u : 0u);
         }
-        if (h == 1) tc_commit(rf_smem_u32(&sm.bar_v_empty[b & 1]));
       };
       auto issue_s = [&](int t) {  // S_1 and S_2 of step t
-        const int b = t >> 1, h = t & 1;
-        const uint64_t dk = dk0 + (uint64_t)(((b & 1) * kTileBytes + h * kHalf) >> 4);
+        const int h = t & 1;
+        const uint64_t dk = dk0 + (uint64_t)((t % kQStages) * (kTileBytes / 2) >> 4);
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk) {
-            const int byte = w * D + kk * 32;
-            const uint32_t off = ((uint32_t)(byte >> 7) * kBoxBytes + (byte & 127)) >> 4;
-            mma_ss(tmem + 192 * h + 64 * w, dq + off, dk + off, id_sd, kk > 0 ? 1u : 0u);
+            const uint32_t byte = w * D + kk * 32, box = byte >> 7, in = byte & 127;
+            mma_ss(tmem + 192 * h + 64 * w, dq + ((box * kBoxBytes + in) >> 4), dk + ((box * kHalfBox + in) >> 4), id_sd,
+                   kk > 0 ? 1u : 0u);
           }
         tc_commit(rf_smem_u32(&sm.bar_sd_full[h]));
       };
-      bool ok = warp_wait<true>(rf_smem_u32(&sm.bar_q), 0, abort) &&
-                warp_wait<true>(rf_smem_u32(&sm.bar_v_full[0]), 0, abort) &&
-                warp_wait<true>(rf_smem_u32(&sm.bar_k_full[0]), 0, abort);
-      if (ok) {
+      bool ok = warp_wait<true>(rf_smem_u32(&sm.bar_q), 0, abort);
+      for (int t = 0; ok && t < 2; ++t) {
+        ok = warp_wait<true>(rf_smem_u32(&sm.bar_full[t]), 0, abort);
+        if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_da(0);
-          issue_s(0);
-          issue_da(1);
-          issue_s(1);
+          issue_da(t);
+          issue_s(t);
         }
         __syncwarp();
       }
       for (int t = 0; ok && t < nt; ++t) {
-        const int b = t >> 1, h = t & 1, st = b & 1;
-        const uint32_t ph = b & 1;  // each half's barriers complete once per block
+        const int h = t & 1, st = t % kQStages;
+        const uint32_t ph = (t >> 1) & 1;  // each half's barriers complete once per block
+        // Every barrier check takes about as long as two MMAs: this one is made
+        // while dS is still being computed.
+        if (t + 2 < nt &&
+            !warp_wait<true>(rf_smem_u32(&sm.bar_full[(t + 2) % kQStages]), ((t + 2) / kQStages) & 1, abort)) {
+          ok = false;
+          break;
+        }
         if (!warp_wait<true>(rf_smem_u32(&sm.bar_ds_full[h]), ph, abort)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t dk = dkn0 + (uint64_t)((st * kTileBytes + h * kHalf) >> 4);
+          const uint64_t dk = dkn0 + (uint64_t)(st * (kTileBytes / 2) >> 4);
 #pragma unroll
           for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_ts(tmem + kDq + 64 * w, tmem + 192 * h + 64 * w + 8 * kk,
-                     dk + (uint64_t)(((D == 128 ? w : 0) * kBoxBytes + kk * 2048) >> 4), id_dq,
+                     dk + (uint64_t)(((D == 128 ? w : 0) * kHalfBox + kk * 2048) >> 4), id_dq,
                      (t > 0 || kk > 0) ? 1u : 0u);
           tc_commit(rf_smem_u32(&sm.bar_dq_done[h]));
-          if (h == 1) tc_commit(rf_smem_u32(&sm.bar_k_empty[st]));
+          tc_commit(rf_smem_u32(&sm.bar_empty[st]));
         }
         __syncwarp();
         if (t + 2 < nt) {
-          const int b2 = b + 1;
-          const uint32_t ph2 = (b2 >> 1) & 1;
-          if (h == 0 && !warp_wait<true>(rf_smem_u32(&sm.bar_v_full[b2 & 1]), ph2, abort)) { ok = false; break; }
-          tc_fence_after();
           if (elect_one()) issue_da(t + 2);
           __syncwarp();
-          if (h == 0 && !warp_wait<true>(rf_smem_u32(&sm.bar_k_full[b2 & 1]), ph2, abort)) { ok = false; break; }
           if (!warp_wait<true>(rf_smem_u32(&sm.bar_dq_done[h]), ph, abort)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) issue_s(t + 2);
@@ -408,23 +409,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t scol = lane_base + 192 * h + 64 * w, acol = lane_base + 192 * h + 128;
     const float* st = a.stats + ((size_t)n * g.t_qblk + tb) * (4 * RF_BLOCK);
-    const float nlse = st[w * RF_BLOCK + r];
+    const float* str = st + (r >> 6) * 256 + (r & 63);
+    const float nlse = str[w * 64];
     const float c = (w == 0 ? 1.f : -a.lambda[n]) * (kBf16 ? 1.f : rf_pow2(es));
-    const float dc = c * st[(2 + w) * RF_BLOCK + r];
+    const float dc = c * str[(2 + w) * 64];
     bool ok = true;
     for (int b = 0; b < nv; ++b) {
       if (!warp_wait(rf_smem_u32(&sm.bar_sd_full[h]), b & 1, abort)) { ok = false; break; }
       tc_fence_after();
       const int vr = (sm.list[b] == s.n_pb - 1) ? vr_last : RF_BLOCK;
+      uint32_t sr[2][16], da[2][16];
+      tmem_ld16(scol, sr[0]);
+      tmem_ld16(acol, da[0]);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t sr[32], da[32], pk[16];
-        tmem_ld32(scol + 32 * x, sr);
-        tmem_ld32(acol + 32 * x, da);
+      for (int x = 0; x < 4; ++x) {
         tmem_wait_ld();
-        if (vr == RF_BLOCK) ds_chunk<kBf16, true>(sr, da, 64 * h + 32 * x, vr, a.sl2, nlse, c, dc, pk);
-        else                ds_chunk<kBf16, false>(sr, da, 64 * h + 32 * x, vr, a.sl2, nlse, c, dc, pk);
-        tmem_st16(scol + 16 * x, pk);
+        tmem_pin16(sr[x & 1]);
+        tmem_pin16(da[x & 1]);
+        if (x < 3) {  // the next 16 columns, on their way while these are computed
+          tmem_ld16(scol + 16 * (x + 1), sr[(x + 1) & 1]);
+          tmem_ld16(acol + 16 * (x + 1), da[(x + 1) & 1]);
+        }
+        uint32_t pk[8];
+        if (vr == RF_BLOCK) ds_chunk<kBf16, true>(sr[x & 1], da[x & 1], 64 * h + 16 * x, vr, a.sl2, nlse, c, dc, pk);
+        else                ds_chunk<kBf16, false>(sr[x & 1], da[x & 1], 64 * h + 16 * x, vr, a.sl2, nlse, c, dc, pk);
+        tmem_st8(scol + 8 * x, pk);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -453,11 +462,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // query rows of one (head, query block) that lists the block: S_w^T and dA^T
 // with N = 64, A^T, dS_w^T from registers, then dV += A^T dO, dK_w += dS_w^T Q_w.
 // TMEM: dV at [256, 256 + D), dK at [384, 512) (per map 64 columns, as dQ), and
-// four 64-column slots in which a step's S_1, S_2 and dA take turns: A and dS_1
-// are written over S_1's slot and dS_2 over S_2's, each thread over columns that
-// it alone has read; S_1 of the next step goes into the free slot while this
-// step's elements are computed, its S_2 into dA's slot as soon as those are
-// done, and its dA into S_1's slot once A and dS_1 have been read.
+// four 64-column slots in which a step's S_1, S_2 and dA take turns.  S_1 of the
+// next step goes into the free slot; its S_2 and dA into dA's and S_1's as soon as
+// this step's numbers are in registers, long before they are used up; dS_1 and
+// dS_2 are written over S_2, each thread over columns that it alone has read, and
+// A^T goes through shared memory (two buffers).  So the elements of a step never
+// wait for its matrix products, and the warpgroups drift apart until one's
+// exponentials run under another's arithmetic.  A barrier check costs its warp
+// 100 to 200 cycles; the two that a step makes are what is left of five.
 // Warpgroup e takes queries [16 e, +16) of the step, which is one 16-wide slice
 // of the reduction of dV and dK.
 // Rows that a query block does not have carry -lse = -inf (P = 0); their Q and
@@ -479,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const RfGeomDev& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gk = blockIdx.x / g.t_qblk, tb = blockIdx.x % g.t_qblk;  // tb: the key block
+  int gk, tb;  // tb: the key block
+  rf_cta_item(g, a.order, g.n2, blockIdx.x, gk, tb);
   const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
   const int group = g.n1 / g.n2;
   int k_r0, k_rows;
@@ -494,15 +507,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(rf_smem_u32(&sm.bar_kv), 1);
     mbar_init(rf_smem_u32(&sm.bar_aux), 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kKvStages; ++i) {
       mbar_init(rf_smem_u32(&sm.bar_full[i]), 1);
       mbar_init(rf_smem_u32(&sm.bar_empty[i]), 1);
-      mbar_init(rf_smem_u32(&sm.bar_s1_full[i]), 1);
     }
-    mbar_init(rf_smem_u32(&sm.bar_s2_full), 1);
+    mbar_init(rf_smem_u32(&sm.bar_s1_full[0]), 2);  // the product's commit, and the issuing warp itself
+    mbar_init(rf_smem_u32(&sm.bar_s1_full[1]), 2);
     mbar_init(rf_smem_u32(&sm.bar_da_full), 1);
+    mbar_init(rf_smem_u32(&sm.bar_read), kCompute);
     mbar_init(rf_smem_u32(&sm.bar_ew), kCompute);
-    mbar_init(rf_smem_u32(&sm.bar_x_done), 1);
     mbar_init(rf_smem_u32(&sm.bar_y_done), 1);
     mbar_init(rf_smem_u32(&sm.bar_final), 1);
     mbar_init(rf_smem_u32(&sm.bar_drain), 1);
@@ -546,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      int it = 0, tails = 0;
+      int t = 0, tails = 0;
       bool ok = true;
       for (int hh = 0; ok && hh < group; ++hh) {
         const int n = gk * group + hh;
@@ -554,54 +567,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t* bw = a.bits + ((size_t)n * g.t_qblk + tb) * a.words;
         for (int wd = 0; ok && wd < a.words; ++wd) {
           uint32_t word = bw[wd];
-          while (word) {
+          while (ok && word) {
             const int qb = wd * 32 + __ffs(word) - 1;
             word &= word - 1;
-            const int st = it & 1;
-            if (it >= 2 && !warp_wait(rf_smem_u32(&sm.bar_empty[st]), ((it >> 1) & 1) ^ 1, abort)) {
-              if (lane == 0) record_timeout(abort, a.status, 8);
-              ok = false;
-              break;
-            }
             int r0, nr;
             rf_block_span(s, qb, r0, nr);
-            const bool tail = nr < RF_BLOCK;
-            const uint32_t bar = rf_smem_u32(tail ? &sm.bar_aux : &sm.bar_full[st]);
-            if (lane == 0) {
-              sm.lam[st] = lam;
-              coords(g.n1, n, r0, c1, c2);
-              mbar_arrive_expect_tx(bar, 2 * kTileBytes + kStatBytes);
-              for (int x = 0; x < kBoxes; ++x) {
-                tma_load_3d(rf_smem_u32(sm.q[st] + x * kBoxBytes), &tm_q, bar, x * 64, c1, c2);
-                tma_load_3d(rf_smem_u32(sm.d_o[st] + x * kBoxBytes), &tm_do, bar, x * 64, c1, c2);
+            for (int h = 0; h < 2; ++h, ++t) {  // 64 rows of the query block each
+              const int st = t % kKvStages;
+              if (t >= kKvStages && !warp_wait(rf_smem_u32(&sm.bar_empty[st]), ((t / kKvStages) & 1) ^ 1, abort)) {
+                if (lane == 0) record_timeout(abort, a.status, 8);
+                ok = false;
+                break;
               }
-              bulk_load(rf_smem_u32(&sm.stats[st][0][0]),
-                        a.stats + ((size_t)n * g.t_qblk + s.qblk_off + qb) * (4 * RF_BLOCK), kStatBytes, bar);
-            }
-            __syncwarp();
-            if (tail) {  // at most one query block per head
-              const bool landed = warp_wait(bar, tails & 1, &no_abort);
-              ++tails;
-              if (landed) {
-                zero_tail(sm.q[st], kBoxes, nr, lane);
-                zero_tail(sm.d_o[st], kBoxes, nr, lane);
-              }
-              fence_async_smem();
-              __syncwarp();
+              const int left = nr - 64 * h;
+              const bool tail = left < 64;
+              const uint32_t bar = rf_smem_u32(tail ? &sm.bar_aux : &sm.bar_full[st]);
               if (lane == 0) {
-                if (!landed) record_timeout(abort, a.status, 8);
-                mbar_arrive(rf_smem_u32(&sm.bar_full[st]));
+                sm.lam[st] = lam;
+                coords(g.n1, n, r0 + 64 * h, c1, c2);
+                mbar_arrive_expect_tx(bar, kTileBytes + kStatBytes);
+                for (int x = 0; x < kBoxes; ++x) {
+                  tma_load_3d(rf_smem_u32(sm.q[st] + x * kHalfBox), &tm_q, bar, x * 64, c1, c2);
+                  tma_load_3d(rf_smem_u32(sm.d_o[st] + x * kHalfBox), &tm_do, bar, x * 64, c1, c2);
+                }
+                bulk_load(rf_smem_u32(&sm.stats[st][0][0]),
+                          a.stats + (((size_t)n * g.t_qblk + s.qblk_off + qb) * 2 + h) * 256, kStatBytes, bar);
               }
               __syncwarp();
+              if (tail) {  // the halves of at most one query block per head
+                const bool landed = warp_wait(bar, tails & 1, &no_abort);
+                ++tails;
+                if (landed) {
+                  zero_tail(sm.q[st], kBoxes, max(left, 0), lane);
+                  zero_tail(sm.d_o[st], kBoxes, max(left, 0), lane);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  if (!landed) record_timeout(abort, a.status, 8);
+                  mbar_arrive(rf_smem_u32(&sm.bar_full[st]));
+                }
+                __syncwarp();
+              }
             }
-            ++it;
           }
         }
       }
       if (*abort) {
         warp_wait(rf_smem_u32(&sm.bar_kv), 0, &no_abort);
-        for (int i = (it > 2 ? it - 2 : 0); i < it; ++i)
-          warp_wait(rf_smem_u32(&sm.bar_full[i & 1]), (i >> 1) & 1, &no_abort);
+        for (int i = (t > kKvStages ? t - kKvStages : 0); i < t; ++i)
+          warp_wait(rf_smem_u32(&sm.bar_full[i % kKvStages]), (i / kKvStages) & 1, &no_abort);
       }
     } else if (warp == kMmaWarp && ni > 0) {
       // ---------------- tcgen05.mma issue ----------------
@@ -613,33 +628,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dv = umma_desc_sw128(rf_smem_u32(sm.v), 16, 1024);
       const uint64_t dq0 = umma_desc_sw128(rf_smem_u32(sm.q[0]), 16, 1024);
       const uint64_t do0 = umma_desc_sw128(rf_smem_u32(sm.d_o[0]), 16, 1024);
-      const uint64_t dqn0 = umma_desc_sw128(rf_smem_u32(sm.q[0]), kBoxBytes, 1024);
-      const uint64_t don0 = umma_desc_sw128(rf_smem_u32(sm.d_o[0]), kBoxBytes, 1024);
+      const uint64_t dqn0 = umma_desc_sw128(rf_smem_u32(sm.q[0]), kHalfBox, 1024);
+      const uint64_t don0 = umma_desc_sw128(rf_smem_u32(sm.d_o[0]), kHalfBox, 1024);
+      const uint64_t da_t = umma_desc_sw128(rf_smem_u32(sm.a[0]), 16, 1024);
       const int nt = 2 * ni;
       // slots of step t: S_1, S_2, dA (the fourth is free for the next S_1)
       auto slot = [&](int t, int which) -> uint32_t {
         const uint32_t tab = which == 0 ? 0x2130u : (which == 1 ? 0x3021u : 0x1302u);
         return tmem + 64u * ((tab >> (4 * (t & 3))) & 15u);
       };
-      auto tile_off = [&](int t) -> uint64_t {  // stage and 64-row half of step t's Q and dO
-        return (uint64_t)((((t >> 1) & 1) * kTileBytes + (t & 1) * kHalf) >> 4);
-      };
+      auto tile_off = [&](int t) -> uint64_t { return (uint64_t)((t % kKvStages) * (kTileBytes / 2) >> 4); };
       auto issue_s = [&](int t, int w) {
         const uint64_t b = dq0 + tile_off(t);
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk) {
-          const int byte = w * D + kk * 32;
-          const uint32_t off = ((uint32_t)(byte >> 7) * kBoxBytes + (byte & 127)) >> 4;
-          mma_ss(slot(t, w), dk + off, b + off, id_s, kk > 0 ? 1u : 0u);
+          const uint32_t byte = w * D + kk * 32, box = byte >> 7, in = byte & 127;
+          mma_ss(slot(t, w), dk + ((box * kBoxBytes + in) >> 4), b + ((box * kHalfBox + in) >> 4), id_s, kk > 0 ? 1u : 0u);
         }
-        tc_commit(rf_smem_u32(w == 0 ? &sm.bar_s1_full[t & 1] : &sm.bar_s2_full));
+        if (w == 0) {
+          // The arrival hands on what this thread has seen: the step's tiles and
+          // numbers in shared memory, and A's buffer read (bar_y_done of t - 2).
+          mbar_arrive(rf_smem_u32(&sm.bar_s1_full[t & 1]));
+          tc_commit(rf_smem_u32(&sm.bar_s1_full[t & 1]));
+        }
       };
       auto issue_da = [&](int t) {
         const uint64_t b = do0 + tile_off(t);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-          mma_ss(slot(t, 2), dv + off, b + off, id_s, kk > 0 ? 1u : 0u);
+          const uint32_t in = (kk & 3) * 32, box = kk >> 2;
+          mma_ss(slot(t, 2), dv + ((box * kBoxBytes + in) >> 4), b + ((box * kHalfBox + in) >> 4), id_s, kk > 0 ? 1u : 0u);
         }
         tc_commit(rf_smem_u32(&sm.bar_da_full));
       };
@@ -657,44 +675,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; ok && t < nt; ++t) {
         const bool more = t + 1 < nt;
         if (more) {
-          const int it1 = (t + 1) >> 1;
-          if (((t + 1) & 1) == 0 &&
-              !warp_wait<true>(rf_smem_u32(&sm.bar_full[it1 & 1]), (it1 >> 1) & 1, abort)) { ok = false; break; }
-          // the slot of S_1(t + 1) held dS_2(t - 1)
+          if (!warp_wait<true>(rf_smem_u32(&sm.bar_full[(t + 1) % kKvStages]), ((t + 1) / kKvStages) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          // the slot of S_1(t + 1) held dS_1(t - 1) and dS_2(t - 1)
           if (t > 0 && !warp_wait<true>(rf_smem_u32(&sm.bar_y_done), (t - 1) & 1, abort)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) issue_s(t + 1, 0);
           __syncwarp();
         }
+        if (more) {
+          if (!warp_wait<true>(rf_smem_u32(&sm.bar_read), t & 1, abort)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            issue_s(t + 1, 1);
+            issue_da(t + 1);
+          }
+          __syncwarp();
+        }
         if (!warp_wait<true>(rf_smem_u32(&sm.bar_ew), t & 1, abort)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
-          if (more) issue_s(t + 1, 1);
           const uint64_t bo = don0 + tile_off(t), bq = dqn0 + tile_off(t);
-          const uint32_t sa = slot(t, 0), sb = slot(t, 1);
+          const uint32_t sb = slot(t, 1);
           const uint32_t acc = t > 0 ? 1u : 0u;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ts(tmem + kDv, sa + 16 * kk, bo + (uint64_t)(kk * 2048 >> 4), id_dv, kk > 0 ? 1u : acc);
+            mma_ss(tmem + kDv, da_t + (uint64_t)(((t & 1) * (RF_BLOCK * 128) + kk * 32) >> 4), bo + (uint64_t)(kk * 2048 >> 4), id_dv, kk > 0 ? 1u : acc);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts(tmem + kDk, sa + 16 * kk + 8, bq + (uint64_t)(kk * 2048 >> 4), id_dk, kk > 0 ? 1u : acc);
-          tc_commit(rf_smem_u32(&sm.bar_x_done));
+          for (int w = 0; w < 2; ++w)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts(tmem + kDk + 64, sb + 16 * kk,
-                   bq + (uint64_t)(((D == 128 ? 1 : 0) * kBoxBytes + kk * 2048) >> 4), id_dk, kk > 0 ? 1u : acc);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(tmem + kDk + 64 * w, sb + 16 * kk + 8 * (1 - w),
+                     bq + (uint64_t)(((D == 128 ? w : 0) * kHalfBox + kk * 2048) >> 4), id_dk, kk > 0 ? 1u : acc);
           tc_commit(rf_smem_u32(&sm.bar_y_done));
-          if (t & 1) tc_commit(rf_smem_u32(&sm.bar_empty[(t >> 1) & 1]));
+          tc_commit(rf_smem_u32(&sm.bar_empty[t % kKvStages]));
         }
         __syncwarp();
-        if (more) {
-          // the slot of dA(t + 1) held A(t) and dS_1(t)
-          if (!warp_wait<true>(rf_smem_u32(&sm.bar_x_done), t & 1, abort)) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) issue_da(t + 1);
-          __syncwarp();
-        }
       }
       if (!ok && lane == 0) record_timeout(abort, a.status, 9);
       if (elect_one()) {
@@ -712,78 +730,97 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint64_t sl = rf_f2(__float_as_uint(a.sl2), __float_as_uint(a.sl2));
     const float up_a = (float)ea, up_s = kBf16 ? 1.f : rf_scale_pow2(1.f, es - ea);
+    const uint64_t ua = rf_f2(__float_as_uint(up_a), __float_as_uint(up_a));
+    const uint64_t us = rf_f2(__float_as_uint(up_s), __float_as_uint(up_s));
+    const uint64_t neg1 = rf_f2(__float_as_uint(-1.f), __float_as_uint(-1.f));
+    const uint32_t stats0 = rf_smem_u32(&sm.stats[0][0][0]) + 64u * e;
+    // this thread's two 16-byte chunks of its key's row of A^T
+    const uint32_t a_row = rf_smem_u32(sm.a[0]) + 128u * r;
+    const uint32_t a_c0 = a_row + 16u * ((2 * e) ^ (r & 7)), a_c1 = a_row + 16u * ((2 * e + 1) ^ (r & 7));
     bool ok = true;
     for (int t = 0; t < 2 * ni; ++t) {
-      const uint32_t ta = 0x2130u, tbb = 0x3021u, tc = 0x1302u;
-      const uint32_t s1c = lane_base + 64u * ((ta >> (4 * (t & 3))) & 15u) + 16 * e;
-      const uint32_t s2c = lane_base + 64u * ((tbb >> (4 * (t & 3))) & 15u) + 16 * e;
-      const uint32_t dac = lane_base + 64u * ((tc >> (4 * (t & 3))) & 15u) + 16 * e;
-      const int st = (t >> 1) & 1, q0 = 64 * (t & 1) + 16 * e;
-      // the item's numbers are visible: its tiles' barrier is the same
-      if ((t & 1) == 0 && !warp_wait(rf_smem_u32(&sm.bar_full[st]), (t >> 2) & 1, abort)) { ok = false; break; }
+      const uint32_t sh = 4 * (t & 3);
+      const uint32_t s1c = lane_base + 64u * ((0x2130u >> sh) & 15u) + 16 * e;
+      const uint32_t s2c = lane_base + 64u * ((0x3021u >> sh) & 15u) + 16 * e;
+      const uint32_t dac = lane_base + 64u * ((0x1302u >> sh) & 15u) + 16 * e;
+      const int st = t % kKvStages;
+      // this thread's 16 queries' numbers: -lse_1, -lse_2, delta_1, delta_2, 256 bytes apart
+      const uint32_t num = stats0 + (uint32_t)st * kStatBytes;
       if (!warp_wait(rf_smem_u32(&sm.bar_s1_full[t & 1]), (t >> 1) & 1, abort)) { ok = false; break; }
-      if (!warp_wait(rf_smem_u32(&sm.bar_s2_full), t & 1, abort)) { ok = false; break; }
       tc_fence_after();
       uint32_t s1[16], s2[16];
       tmem_ld16(s1c, s1);
-      tmem_ld16(s2c, s2);
       tmem_wait_ld();
-      const float nlam = -sm.lam[st];
-      const uint64_t nl2 = rf_f2(__float_as_uint(nlam), __float_as_uint(nlam));
-      const uint64_t ua = rf_f2(__float_as_uint(up_a), __float_as_uint(up_a));
-      const uint64_t us = rf_f2(__float_as_uint(up_s), __float_as_uint(up_s));
-      uint32_t out[16];  // A in [0, 8), dS_1 in [8, 16)
-      uint32_t out2[8];
-      const float* l1 = sm.stats[st][0] + q0;
-      const float* l2 = sm.stats[st][1] + q0;
+      tmem_pin16(s1);
+      auto exps = [&](uint32_t* x, uint32_t nl) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        uint64_t x = rf_fma2(rf_f2(s1[i], s1[i + 1]), sl, *reinterpret_cast<const uint64_t*>(l1 + i));
-        uint64_t y = rf_fma2(rf_f2(s2[i], s2[i + 1]), sl, *reinterpret_cast<const uint64_t*>(l2 + i));
-        if constexpr (!kBf16) {
-          x = rf_add2(x, ua);
-          y = rf_add2(y, ua);
+        for (int i = 0; i < 16; i += 4) {
+          uint64_t l0, l1;
+          lds_2x2(nl + 4 * i, l0, l1);
+          uint64_t y0 = rf_fma2(rf_f2(x[i], x[i + 1]), sl, l0), y1 = rf_fma2(rf_f2(x[i + 2], x[i + 3]), sl, l1);
+          if constexpr (!kBf16) {
+            y0 = rf_add2(y0, ua);
+            y1 = rf_add2(y1, ua);
+          }
+          float f0, f1, f2, f3;
+          rf_f2_split(y0, f0, f1);
+          rf_f2_split(y1, f2, f3);
+          x[i] = __float_as_uint(rf_ex2(f0));
+          x[i + 1] = __float_as_uint(rf_ex2(f1));
+          x[i + 2] = __float_as_uint(rf_ex2(f2));
+          x[i + 3] = __float_as_uint(rf_ex2(f3));
         }
-        float x0, x1, y0, y1;
-        rf_f2_split(x, x0, x1);
-        rf_f2_split(y, y0, y1);
-        const uint64_t p1 = rf_f2(__float_as_uint(rf_ex2(x0)), __float_as_uint(rf_ex2(x1)));
-        const uint64_t p2 = rf_mul2(nl2, rf_f2(__float_as_uint(rf_ex2(y0)), __float_as_uint(rf_ex2(y1))));
-        float a0, a1;
-        rf_f2_split(rf_add2(p1, p2), a0, a1);
-        out[i >> 1] = rf_pack2<kBf16>(a0, a1);
-        rf_f2_split(p1, x0, x1);
-        rf_f2_split(p2, y0, y1);
-        s1[i] = __float_as_uint(x0);
-        s1[i + 1] = __float_as_uint(x1);
-        s2[i] = __float_as_uint(y0);
-        s2[i + 1] = __float_as_uint(y1);
-      }
+      };
+      exps(s1, num);  // P_1, while S_2 and dA are still being computed
       if (!warp_wait(rf_smem_u32(&sm.bar_da_full), t & 1, abort)) { ok = false; break; }
       tc_fence_after();
       uint32_t da[16];
+      tmem_ld16(s2c, s2);
       tmem_ld16(dac, da);
       tmem_wait_ld();
-      const float* d1 = sm.stats[st][2] + q0;
-      const float* d2 = sm.stats[st][3] + q0;
-      const uint64_t neg1 = rf_f2(__float_as_uint(-1.f), __float_as_uint(-1.f));
+      tmem_pin16(s2);
+      tmem_pin16(da);
+      tc_fence_before();
+      mbar_arrive(rf_smem_u32(&sm.bar_read));
+      exps(s2, num + 256);
+      const float nlam = -lds_f(rf_smem_u32(&sm.lam[0]) + 4u * st);
+      const uint64_t nl2 = rf_f2(__float_as_uint(nlam), __float_as_uint(nlam));
+      uint32_t out[16];  // A in [0, 8) for now; dS_2 in [0, 8) and dS_1 in [8, 16)
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
-        const uint64_t dd = rf_f2(da[i], da[i + 1]);
-        uint64_t t1 = rf_fma2(*reinterpret_cast<const uint64_t*>(d1 + i), neg1, dd);
-        uint64_t t2 = rf_fma2(*reinterpret_cast<const uint64_t*>(d2 + i), neg1, dd);
-        if constexpr (!kBf16) {
-          t1 = rf_mul2(t1, us);
-          t2 = rf_mul2(t2, us);
-        }
-        float y0, y1;
-        rf_f2_split(rf_mul2(rf_f2(s1[i], s1[i + 1]), t1), y0, y1);
-        out[8 + (i >> 1)] = rf_pack2<kBf16>(y0, y1);
-        rf_f2_split(rf_mul2(rf_f2(s2[i], s2[i + 1]), t2), y0, y1);
-        out2[i >> 1] = rf_pack2<kBf16>(y0, y1);
+        const uint64_t p2 = rf_mul2(nl2, rf_f2(s2[i], s2[i + 1]));
+        float a0, a1;
+        rf_f2_split(rf_add2(rf_f2(s1[i], s1[i + 1]), p2), a0, a1);
+        out[i >> 1] = rf_pack2<kBf16>(a0, a1);
+        rf_f2_split(p2, a0, a1);
+        s2[i] = __float_as_uint(a0);
+        s2[i + 1] = __float_as_uint(a1);
       }
-      tmem_st16(s1c, out);
-      tmem_st8(s2c, out2);
+      sts128(a_c0 + (t & 1) * (RF_BLOCK * 128), out);
+      sts128(a_c1 + (t & 1) * (RF_BLOCK * 128), out + 4);
+      fence_async_smem();
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        uint64_t d1[2], d2[2];
+        lds_2x2(num + 512 + 4 * i, d1[0], d1[1]);
+        lds_2x2(num + 768 + 4 * i, d2[0], d2[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = i + 2 * k;
+          const uint64_t dd = rf_f2(da[c], da[c + 1]);
+          uint64_t t1 = rf_fma2(d1[k], neg1, dd), t2 = rf_fma2(d2[k], neg1, dd);
+          if constexpr (!kBf16) {
+            t1 = rf_mul2(t1, us);
+            t2 = rf_mul2(t2, us);
+          }
+          float y0, y1;
+          rf_f2_split(rf_mul2(rf_f2(s1[c], s1[c + 1]), t1), y0, y1);
+          out[8 + (c >> 1)] = rf_pack2<kBf16>(y0, y1);
+          rf_f2_split(rf_mul2(rf_f2(s2[c], s2[c + 1]), t2), y0, y1);
+          out[c >> 1] = rf_pack2<kBf16>(y0, y1);
+        }
+      }
+      tmem_st16(s2c, out);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(rf_smem_u32(&sm.bar_ew));
@@ -887,10 +924,11 @@ __global__ void __launch_bounds__(256)
     }
     sum2 += e2;
     if (lane == 0) {
-      st[r] = r < nrows ? -lse[(size_t)n * rows_total + lrow + r] : -INFINITY;
-      st[RF_BLOCK + r] = r < nrows ? -lse[((size_t)g.n1 + n) * rows_total + lrow + r] : -INFINITY;
-      st[2 * RF_BLOCK + r] = e1;
-      st[3 * RF_BLOCK + r] = e2;
+      float* o = st + (r >> 6) * 256 + (r & 63);
+      o[0] = r < nrows ? -lse[(size_t)n * rows_total + lrow + r] : -INFINITY;
+      o[64] = r < nrows ? -lse[((size_t)g.n1 + n) * rows_total + lrow + r] : -INFINITY;
+      o[128] = e1;
+      o[192] = e2;
     }
   }
   if (lane == 0) part[warp] = sum2;
@@ -940,12 +978,16 @@ rf_status_t launch_t(const rf_plan* p, const BwdArgs& a, const void* q_r, const 
   const RfGeomDev& g = p->g;
   const long long gq = (long long)g.t_qblk * g.n1, gkv = (long long)g.t_qblk * g.n2;
   if (gq + gkv > 0x7FFFFFFFll) return rf_fail(RF_ERR_INVALID_ARG, "grid too large");
-  CUtensorMap mq, mk, mv, mo;
+  // [0]: 128-row boxes (the tiles a CTA keeps), [1]: 64-row boxes (those it streams)
+  CUtensorMap mq[2], mk[2], mv[2], mo[2];
   rf_status_t s;
-  if ((s = make_map(&mq, p, q_r, g.n1, kElemPlan)) != RF_OK) return s;
-  if ((s = make_map(&mk, p, k_r, g.n2, kElemPlan)) != RF_OK) return s;
-  if ((s = make_map(&mv, p, v_r, g.n2, kElemPlan)) != RF_OK) return s;
-  if ((s = make_map(&mo, p, do_r, g.n1, kElemPlan)) != RF_OK) return s;
+  for (int i = 0; i < 2; ++i) {
+    const int rows = i ? 64 : RF_BLOCK;
+    if ((s = make_map(&mq[i], p, q_r, g.n1, kElemPlan, rows)) != RF_OK) return s;
+    if ((s = make_map(&mk[i], p, k_r, g.n2, kElemPlan, rows)) != RF_OK) return s;
+    if ((s = make_map(&mv[i], p, v_r, g.n2, kElemPlan, rows)) != RF_OK) return s;
+    if ((s = make_map(&mo[i], p, do_r, g.n1, kElemPlan, rows)) != RF_OK) return s;
+  }
   size_t sq = sizeof(DqSmem<D>) + 1024, skv = sizeof(DkvSmem<D>) + 1024;
   if (sq < 120 * 1024) sq = 120 * 1024;    // each CTA takes all 512 TMEM columns: one per SM
   if (skv < 120 * 1024) skv = 120 * 1024;
@@ -964,9 +1006,9 @@ rf_status_t launch_t(const rf_plan* p, const BwdArgs& a, const void* q_r, const 
   if ((s = rf_check_launch("rf_diff_prep_bwd_kernel")) != RF_OK) return s;
   rf_diff_dlam_kernel<<<(unsigned)g.n1, 256, 0, st>>>(dlam_part, g.t_qblk, dlambda);
   if ((s = rf_check_launch("rf_diff_dlam_kernel")) != RF_OK) return s;
-  kkv<<<(unsigned)gkv, kThreads, skv, st>>>(mq, mk, mv, mo, a);
+  kkv<<<(unsigned)gkv, kThreads, skv, st>>>(mq[1], mk[0], mv[0], mo[1], a);
   if ((s = rf_check_launch("rf_diff_dkv_kernel")) != RF_OK) return s;
-  kq<<<(unsigned)gq, kThreads, sq, st>>>(mq, mk, mv, mo, a);
+  kq<<<(unsigned)gq, kThreads, sq, st>>>(mq[0], mk[1], mv[1], mo[0], a);
   return rf_check_launch("rf_diff_dq_kernel");
 }
 
@@ -985,6 +1027,7 @@ rf_status_t rf_launch_diff_bwd(const rf_plan* p, const void* q_r, const void* k_
   uint32_t* amax = reinterpret_cast<uint32_t*>(w + lay.amax);
   BwdArgs a;
   a.g = p->g;
+  a.order = rf_order(p->g);
   a.sel_idx = sel_idx;
   a.sel_num = sel_num;
   a.lambda = lambda;

@@ -103,12 +103,14 @@ __device__ __forceinline__ float sub_sum(float v, int lanes) {
   return v;
 }
 
-// One row per sub-warp of `lanes` lanes, NV vectors of VEC channels per lane;
-// blockIdx.y = group, so that gamma, beta and (backward) the channels' sums stay
-// in registers over all rows of the CTA's slice.
+// One row at a time per sub-warp of `lanes` lanes, NV vectors of VEC channels per
+// lane, kRows rows loaded before the first is used; blockIdx.y = group, so that
+// gamma, beta and (backward) the channels' sums stay in registers over all rows
+// of the CTA's slice.
 template <class T, int VEC, int NV, bool kBwd>
-__global__ void __launch_bounds__(kThreads) rf_norm_row_kernel(const __grid_constant__ NormArgs a, int lanes) {
+__global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? 4 : 1) rf_norm_row_kernel(const __grid_constant__ NormArgs a, int lanes) {
   constexpr int E = VEC * NV;
+  constexpr int kRows = E <= 8 ? (kBwd ? 2 : 4) : 1;
   const int g = blockIdx.y, lane = threadIdx.x % lanes, sub = threadIdx.x / lanes, subs = kThreads / lanes;
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
@@ -129,67 +131,79 @@ __global__ void __launch_bounds__(kThreads) rf_norm_row_kernel(const __grid_cons
   const float inv = 1.0f / (float)a.width;
   const long long per = (a.n_rows + a.slices - 1) / a.slices;
   const long long first = (long long)blockIdx.x * per, last = min(a.n_rows, first + per);
+  // batch element and row of this sub-warp's next row, carried along
+  long long b = (first + sub) / a.rows, r = (first + sub) - b * a.rows;
   // every lane of a warp runs the same number of turns (the sums use the whole warp)
-  for (long long base = first; base < last; base += subs) {
-    const long long i = base + sub;
-    const bool live = i < last;
-    const long long ii = live ? i : last - 1;
-    const long long b = ii / a.rows, r = ii - b * a.rows;
-    const long long xo = b * a.xs_b + r * a.xs_r + g * a.xs_g, yo = b * a.ys_b + r * a.ys_r + g * a.ys_g;
-    float xv[E], dv[kBwd ? E : 1];
+  for (long long base = first; base < last; base += (long long)subs * kRows) {
+    float xv[kRows][E], dv[kBwd ? kRows : 1][kBwd ? E : 1];
+    long long xo[kRows], yo[kRows];
+    bool live[kRows];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (have[v]) {
-        load_v<T, VEC>(x + xo + (v * lanes + lane) * VEC, xv + v * VEC);
-        if constexpr (kBwd) load_v<T, VEC>(dy + yo + (v * lanes + lane) * VEC, dv + v * VEC);
-      } else {
+    for (int w = 0; w < kRows; ++w) {
+      live[w] = base + sub + (long long)w * subs < last;
+      xo[w] = b * a.xs_b + r * a.xs_r + g * a.xs_g;
+      yo[w] = b * a.ys_b + r * a.ys_r + g * a.ys_g;
+      r += subs;
+      while (r >= a.rows) {
+        r -= a.rows;
+        ++b;
+      }
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          xv[v * VEC + k] = 0.f;
-          if constexpr (kBwd) dv[v * VEC + k] = 0.f;
+      for (int v = 0; v < NV; ++v) {
+        if (have[v] && live[w]) {
+          load_v<T, VEC>(x + xo[w] + (v * lanes + lane) * VEC, xv[w] + v * VEC);
+          if constexpr (kBwd) load_v<T, VEC>(dy + yo[w] + (v * lanes + lane) * VEC, dv[w] + v * VEC);
+        } else {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            xv[w][v * VEC + k] = 0.f;
+            if constexpr (kBwd) dv[w][v * VEC + k] = 0.f;
+          }
         }
       }
     }
-    float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < E; ++k) s += xv[k];
-    const float mu = sub_sum(s, lanes) * inv;
-    s = 0.f;
+    for (int w = 0; w < kRows; ++w) {
+      float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int k = v * VEC; k < (v + 1) * VEC; ++k) {
-        xv[k] = have[v] ? xv[k] - mu : 0.f;
-        s = fmaf(xv[k], xv[k], s);
-      }
-    const float rstd = rsqrtf(sub_sum(s, lanes) * inv + a.eps);
-    if constexpr (!kBwd) {
-#pragma unroll
-      for (int k = 0; k < E; ++k) xv[k] = act_f(fmaf(xv[k] * rstd, gm[k], bt[k]), a.act);
-    } else {
-      float m1 = 0.f, m2 = 0.f;
-#pragma unroll
-      for (int k = 0; k < E; ++k) {
-        xv[k] *= rstd;
-        const float gz = dv[k] * act_d(fmaf(xv[k], gm[k], bt[k]), a.act);
-        if (live) {
-          sg[k] = fmaf(gz, xv[k], sg[k]);
-          sb[k] += gz;
-        }
-        dv[k] = gz * gm[k];
-        m1 += dv[k];
-        m2 = fmaf(dv[k], xv[k], m2);
-      }
-      m1 = sub_sum(m1, lanes) * inv;
-      m2 = sub_sum(m2, lanes) * inv;
-#pragma unroll
-      for (int k = 0; k < E; ++k) xv[k] = rstd * (dv[k] - m1 - xv[k] * m2);
-    }
-    if (live) {
-      const long long oo = kBwd ? xo : yo;
+      for (int k = 0; k < E; ++k) s += xv[w][k];
+      const float mu = sub_sum(s, lanes) * inv;
+      s = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        if (have[v]) store_v<T, VEC>(y + oo + (v * lanes + lane) * VEC, xv + v * VEC);
+#pragma unroll
+        for (int k = v * VEC; k < (v + 1) * VEC; ++k) {
+          xv[w][k] = have[v] ? xv[w][k] - mu : 0.f;
+          s = fmaf(xv[w][k], xv[w][k], s);
+        }
+      const float rstd = rsqrtf(sub_sum(s, lanes) * inv + a.eps);
+      if constexpr (!kBwd) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) xv[w][k] = act_f(fmaf(xv[w][k] * rstd, gm[k], bt[k]), a.act);
+      } else {
+        float m1 = 0.f, m2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          xv[w][k] *= rstd;
+          // a row past the end has dy = 0, and so g = 0, unless eps = 0 makes its xh NaN
+          const float gz = live[w] ? dv[w][k] * act_d(fmaf(xv[w][k], gm[k], bt[k]), a.act) : 0.f;
+          sg[k] = live[w] ? fmaf(gz, xv[w][k], sg[k]) : sg[k];
+          sb[k] += gz;
+          dv[w][k] = gz * gm[k];
+          m1 += dv[w][k];
+          m2 = fmaf(dv[w][k], xv[w][k], m2);
+        }
+        m1 = sub_sum(m1, lanes) * inv;
+        m2 = sub_sum(m2, lanes) * inv;
+#pragma unroll
+        for (int k = 0; k < E; ++k) xv[w][k] = rstd * (dv[w][k] - m1 - xv[w][k] * m2);
+      }
+      if (live[w]) {
+        const long long oo = kBwd ? xo[w] : yo[w];
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (have[v]) store_v<T, VEC>(y + oo + (v * lanes + lane) * VEC, xv[w] + v * VEC);
+      }
     }
   }
   if constexpr (kBwd) {
@@ -223,8 +237,8 @@ __global__ void __launch_bounds__(kThreads) rf_norm_row_kernel(const __grid_cons
 // Channel vector `cv` of VEC channels: element offset of its first channel (a
 // vector never crosses a group unless the groups are contiguous).
 __device__ __forceinline__ long long chan_off(long long c, int width, long long sg) {
-  const long long g = c / width;
-  return g * sg + (c - g * width);
+  const int g = (int)c / width;  // check_desc keeps groups * width below 2^31
+  return g * sg + ((int)c - g * width);
 }
 
 // Per-channel partial sums of one slice of rows.  Forward: {sum(x - x0) as a
@@ -252,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) rf_norm_partial_kernel(const __grid_
     } else {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        const long long g = (c + k) / a.width;
+        const int g = (int)(c + k) / a.width;
         gm[k] = load_p(a.gamma, a.pdt, c + k);
         bt[k] = load_p(a.beta, a.pdt, c + k);
         mu[k] = a.stats[2 * (b * (long long)a.groups + g)];
@@ -260,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) rf_norm_partial_kernel(const __grid_
       }
     }
     const T* dy = static_cast<const T*>(a.dy) + (kBwd ? b * a.ys_b + chan_off(c, a.width, a.ys_g) : 0);
-#pragma unroll 4
+#pragma unroll 8
     for (long long r = first + rl; r < last; r += lanes) {
       float xv[VEC];
       load_v<T, VEC>(x + r * a.xs_r, xv);
@@ -342,37 +356,36 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 }
 
 // Forward: a (batch, group)'s mean and 1 / sqrt(var + eps) from its channels'
-// slices.  Means first, deviations about the common mean after.
+// slices, about one of the slices' means (so that what cancels in the variance
+// is only how far the channels' means lie apart, which is part of it).
 __global__ void __launch_bounds__(kThreads) rf_norm_stats_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float red[kThreads / 32];
   const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
   const long long ch = (long long)a.groups * a.width;
   const float* w = a.ws + (long long)b * a.slices * 2 * ch + (long long)g * a.width;
-  const long long per = (a.rows + a.slices - 1) / a.slices;
-  const float total = (float)a.rows * (float)a.width;
-  const long long items = (long long)a.slices * a.width;
-  auto count = [&](long long sl) { return (float)max(0ll, min(a.rows - sl * per, per)); };
-  const float ref = w[0];  // sums about a value of the data
-  float s = 0.f;
-  for (long long i = threadIdx.x; i < items; i += kThreads) {
-    const long long sl = i / a.width, c = i - sl * a.width;
-    const float n = count(sl);
-    if (n > 0.f) s = fmaf(n, w[sl * 2 * ch + c] - ref, s);
-  }
-  const float mu = ref + block_sum(s, red) / total;
-  s = 0.f;
-  for (long long i = threadIdx.x; i < items; i += kThreads) {
-    const long long sl = i / a.width, c = i - sl * a.width;
-    const float n = count(sl);
-    if (n > 0.f) {
-      const float d = w[sl * 2 * ch + c] - mu;
-      s += w[sl * 2 * ch + ch + c] + n * d * d;
-    }
-  }
-  const float var = block_sum(s, red) / total;
+  const int per = (int)((a.rows + a.slices - 1) / a.slices);
+  const float inv = 1.0f / ((float)a.rows * (float)a.width);
+  const float ref = w[0];
+  float s = 0.f, q = 0.f;
+  const int stride = kThreads / min(a.width, kThreads);  // slices in parallel
+  const int c0 = threadIdx.x % min(a.width, kThreads), s0 = threadIdx.x / min(a.width, kThreads);
+  if (s0 < stride)
+    for (int c = c0; c < a.width; c += kThreads)
+#pragma unroll 8
+      for (int sl = s0; sl < a.slices; sl += stride) {
+        const long long left = a.rows - (long long)sl * per;
+        if (left > 0) {
+          const float n = (float)min(left, (long long)per);
+          const float d = w[sl * 2 * ch + c] - ref, m2 = w[sl * 2 * ch + ch + c];
+          s = fmaf(n, d, s);
+          q += fmaf(n * d, d, m2);
+        }
+      }
+  s = block_sum(s, red) * inv;
+  q = block_sum(q, red) * inv;
   if (threadIdx.x == 0) {
-    a.stats[2 * blockIdx.x] = mu;
-    a.stats[2 * blockIdx.x + 1] = rsqrtf(var + a.eps);
+    a.stats[2 * blockIdx.x] = ref + s;
+    a.stats[2 * blockIdx.x + 1] = rsqrtf(fmaxf(q - s * s, 0.f) + a.eps);
   }
 }
 
@@ -384,14 +397,21 @@ __global__ void __launch_bounds__(kThreads) rf_norm_means_kernel(const __grid_co
   const long long ch = (long long)a.groups * a.width;
   const float* w = a.ws + (long long)b * a.slices * 2 * ch + (long long)g * a.width;
   const float inv = 1.0f / ((float)a.rows * (float)a.width);
-  const long long items = (long long)a.slices * a.width;
   float s0 = 0.f, s1 = 0.f;
-  for (long long i = threadIdx.x; i < items; i += kThreads) {
-    const long long sl = i / a.width, c = i - sl * a.width;
-    const float gm = load_p(a.gamma, a.pdt, (long long)g * a.width + c);
-    s0 = fmaf(gm, w[sl * 2 * ch + c], s0);
-    s1 = fmaf(gm, w[sl * 2 * ch + ch + c], s1);
-  }
+  const int stride = kThreads / min(a.width, kThreads);
+  const int c0 = threadIdx.x % min(a.width, kThreads), l0 = threadIdx.x / min(a.width, kThreads);
+  if (l0 < stride)
+    for (int c = c0; c < a.width; c += kThreads) {
+      float t0 = 0.f, t1 = 0.f;
+#pragma unroll 8
+      for (int sl = l0; sl < a.slices; sl += stride) {
+        t0 += w[sl * 2 * ch + c];
+        t1 += w[sl * 2 * ch + ch + c];
+      }
+      const float gm = load_p(a.gamma, a.pdt, (long long)g * a.width + c);
+      s0 = fmaf(gm, t0, s0);
+      s1 = fmaf(gm, t1, s1);
+    }
   s0 = block_sum(s0, red);
   s1 = block_sum(s1, red);
   if (threadIdx.x == 0) {
@@ -412,6 +432,7 @@ __global__ void __launch_bounds__(kThreads) rf_norm_params_kernel(const float* _
   const long long c = (long long)blockIdx.x * 32 + cl;
   float s0 = 0.f, s1 = 0.f;
   if (c < ch)
+#pragma unroll 8
     for (long long p = pl; p < parts; p += 8) {
       s0 += ws[p * 2 * ch + c];
       s1 += ws[p * 2 * ch + ch + c];
@@ -441,7 +462,7 @@ __global__ void __launch_bounds__(kThreads) rf_norm_apply_kernel(const __grid_co
   float gm[VEC], bt[VEC], mu[VEC], rs[VEC], m1[kBwd ? VEC : 1], m2[kBwd ? VEC : 1];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) {
-    const long long at = 2 * (b * (long long)a.groups + (c + k) / a.width);
+    const long long at = 2 * (b * (long long)a.groups + (int)(c + k) / a.width);
     gm[k] = load_p(a.gamma, a.pdt, c + k);
     bt[k] = load_p(a.beta, a.pdt, c + k);
     mu[k] = a.stats[at];
@@ -458,7 +479,7 @@ __global__ void __launch_bounds__(kThreads) rf_norm_apply_kernel(const __grid_co
   T* out = static_cast<T*>(a.y) + (kBwd ? xo : yo);
   const long long os = kBwd ? a.xs_r : a.ys_r;
   const long long step = (long long)gridDim.x * lanes;
-#pragma unroll 2
+#pragma unroll 4
   for (long long r = (long long)blockIdx.x * lanes + rl; r < a.rows; r += step) {
     float xv[VEC];
     load_v<T, VEC>(x + r * a.xs_r, xv);
@@ -497,6 +518,8 @@ rf_status_t check_desc(const rf_norm_desc_t* d) {
   if (d->batch > 65535 && d->span == RF_NORM_SAMPLE)
     return rf_fail(RF_ERR_UNSUPPORTED, "more than 65535 samples");
   if (d->groups > 65535) return rf_fail(RF_ERR_UNSUPPORTED, "more than 65535 groups");
+  if ((int64_t)d->groups * d->width > (1 << 30)) return rf_fail(RF_ERR_UNSUPPORTED, "too many channels");
+  if (d->rows > (1ll << 30) || d->batch * d->rows > (1ll << 40)) return rf_fail(RF_ERR_UNSUPPORTED, "too many rows");
   const int64_t st[] = {d->x_stride_b, d->x_stride_r, d->x_stride_g, d->y_stride_b, d->y_stride_r, d->y_stride_g};
   for (int64_t s : st)
     if (s < 0) return rf_fail(RF_ERR_INVALID_ARG, "negative stride");
@@ -522,17 +545,17 @@ bool vector_ok(const rf_norm_desc_t* d, bool rows, const void* a, const void* b,
   return true;
 }
 
-// Row slices.  Rows: about six CTAs per SM over all groups, at least a few rows
-// per sub-warp; samples: about four CTAs per SM, at least 32 rows each.
+// Row slices.  Rows: four CTAs per SM over all groups (one wave), at least 32 rows each;
+// samples: two CTAs per SM, at least 32 rows each.
 int slices_of(const rf_norm_desc_t* d) {
   if (d->span == RF_NORM_ROW) {
     const int64_t n = d->batch * d->rows;
-    const int64_t want = (148 * 6 + d->groups - 1) / d->groups, most = (n + 31) / 32;
+    const int64_t want = std::max(1, 148 * 4 / d->groups), most = (n + 31) / 32;
     return (int)std::max<int64_t>(1, std::min(want, most));
   }
   const int64_t b = std::max<int64_t>(1, d->batch);
   const int64_t tiles = ((int64_t)d->groups * d->width + 2047) / 2048;
-  const int64_t want = (148 * 4 + b * tiles - 1) / (b * tiles), most = (d->rows + 31) / 32;
+  const int64_t want = std::max<int64_t>(1, 148 * 2 / (b * tiles)), most = (d->rows + 31) / 32;
   return (int)std::max<int64_t>(1, std::min(want, most));
 }
 
@@ -610,7 +633,7 @@ rf_status_t run_samples_v(const NormArgs& a, cudaStream_t st) {
   else      rf_norm_stats_kernel<<<(unsigned)(a.batch * a.groups), kThreads, 0, st>>>(a);
   if ((s = rf_check_launch("rf_norm_stats_kernel")) != RF_OK) return s;
   const long long lanes = kThreads / tile;
-  const long long most = (a.rows + lanes - 1) / lanes, want = (148ll * 8 + tiles * a.batch - 1) / (tiles * a.batch);
+  const long long most = (a.rows + lanes - 1) / lanes, want = std::max<long long>(1, 148ll * 4 / ((long long)tiles * a.batch));
   const unsigned gx = (unsigned)std::max<long long>(1, std::min(most, want));
   rf_norm_apply_kernel<T, VEC, kBwd><<<dim3(gx, tiles, (unsigned)a.batch), kThreads, 0, st>>>(a, tile);
   return rf_check_launch("rf_norm_apply_kernel");

@@ -47,6 +47,41 @@ __device__ __forceinline__ float row_max(const uint32_t* sr, int vr) {
   return rf_max3(rf_max3(m[0], m[1], m[2]), rf_max3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
 
+// Order of the CTAs of a launch over (head, block): first the blocks that the
+// ranking keeps dense (prefix and first frame; all of a short sequence) of every
+// head, then the others, each class head-major.  A dense block's list is several
+// times as long as a sparse one's, and one that starts late would run on alone.
+struct RfOrder {
+  int n_dense;  // dense blocks of all sequences
+};
+__device__ __forceinline__ int rf_dense_blocks(const RfSeqDev& s) { return s.dense ? s.n_pb + s.nb : s.n_pb + s.ns; }
+__device__ __forceinline__ void rf_cta_item(const RfGeomDev& g, const RfOrder& o, int heads, int bid, int& head, int& tb) {
+  const bool dense = bid < heads * o.n_dense;
+  if (!dense) bid -= heads * o.n_dense;
+  const int per = dense ? o.n_dense : g.t_qblk - o.n_dense;
+  head = bid / per;
+  int i = bid - head * per;
+  tb = 0;
+#pragma unroll 1
+  for (int k = 0; k < g.n_seqs; ++k) {
+    const int nd = rf_dense_blocks(g.seq[k]);
+    const int here = dense ? nd : g.seq[k].n_pb + g.seq[k].nb - nd;
+    if (i < here) {
+      tb = g.seq[k].qblk_off + (dense ? i : nd + i);
+      break;
+    }
+    i -= here;
+  }
+}
+inline RfOrder rf_order(const RfGeomDev& g) {
+  RfOrder o{0};
+  for (int k = 0; k < g.n_seqs; ++k) {
+    const RfSeqDev& s = g.seq[k];
+    o.n_dense += s.dense ? s.n_pb + s.nb : s.n_pb + s.ns;
+  }
+  return o;
+}
+
 // Compacts the `num` entries of a selectIdx row in `list` (shared memory) in
 // place, by one warp: in-range entries that are larger than every in-range
 // entry before them stay, -1 is an unused slot, and anything else (out of
