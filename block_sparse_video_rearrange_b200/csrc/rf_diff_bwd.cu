@@ -87,10 +87,10 @@ struct __align__(1024) DqSmem {
   uint8_t k[kQStages][kTileBytes / 2];
   uint8_t v[kQStages][kTileBytes / 2];
   uint64_t bar_q, bar_aux;
-  uint64_t bar_full[kQStages], bar_empty[kQStages];
-  uint64_t bar_sd_full[2];  // S_1, S_2 and dA of a 64-key half computed
-  uint64_t bar_ds_full[2];  // dS_1 and dS_2 of it stored (and all of S, dA read)
-  uint64_t bar_dq_done[2];  // dQ += dS K of it complete
+  uint64_t bar_full[kQStages];  // step t's tiles landed, and its TMEM columns free (dQ of t - 2 complete)
+  uint64_t bar_empty[kQStages];
+  uint64_t bar_sd_full[2];  // S_1, S_2 and dA of a step computed, by parity
+  uint64_t bar_ds_full[2];  // dS_1 and dS_2 of it stored, by parity
   uint64_t bar_final, bar_drain;
   uint32_t tmem_base;
   int abort;
@@ -109,12 +109,11 @@ struct __align__(1024) DkvSmem {
   float stats[kKvStages][4][64];
   float lam[kKvStages];
   uint64_t bar_kv, bar_aux;
-  uint64_t bar_full[kKvStages], bar_empty[kKvStages];
-  uint64_t bar_s1_full[2];  // S_1 computed, the rows' numbers there, A's buffer free; by parity, one step ahead
-  uint64_t bar_da_full;     // S_2 and dA computed
-  uint64_t bar_read;        // S_1, S_2 and dA of a step read into registers
-  uint64_t bar_ew;          // A, dS_1, dS_2 of a step stored
-  uint64_t bar_y_done;      // and read by their products
+  uint64_t bar_full[kKvStages];  // step t's tiles landed, and A's buffer and dS's slot free (products of t - 2)
+  uint64_t bar_empty[kKvStages];
+  uint64_t bar_sd_full;  // S_1, S_2 and dA of a step computed, the rows' numbers there
+  uint64_t bar_read;     // and read into registers
+  uint64_t bar_ew[2];    // A, dS_1, dS_2 of a step stored, by parity
   uint64_t bar_final, bar_drain;
   uint32_t tmem_base;
   int abort;
@@ -133,7 +132,7 @@ __device__ __forceinline__ void zero_tail(uint8_t* tile, int boxes, int nrows, i
 // dS of 16 keys of one map for one query row: P = 2^(s * sl2 + nlse), then
 // P * (dA * c - dc), rounded to 16 bits and packed.
 template <bool kBf16, bool kFull>
-__device__ __forceinline__ void ds_chunk(const uint32_t* s, const uint32_t* da, int c0, int vr, float sl2,
+__device__ __forceinline__ void ds_chunk(const uint32_t* s, const uint32_t* da, int vr, float sl2,
                                          float nlse, float c, float dc, uint32_t* pk) {
   const uint64_t sl = rf_f2(__float_as_uint(sl2), __float_as_uint(sl2));
   const uint64_t nl = rf_f2(__float_as_uint(nlse), __float_as_uint(nlse));
@@ -146,8 +145,8 @@ __device__ __forceinline__ void ds_chunk(const uint32_t* s, const uint32_t* da, 
     const uint64_t p = rf_f2(__float_as_uint(rf_ex2(x0)), __float_as_uint(rf_ex2(x1)));
     rf_f2_split(rf_mul2(p, rf_fma2(rf_f2(da[i], da[i + 1]), cc, nd)), y0, y1);
     if (!kFull) {
-      y0 = c0 + i < vr ? y0 : 0.f;
-      y1 = c0 + i + 1 < vr ? y1 : 0.f;
+      y0 = i < vr ? y0 : 0.f;
+      y1 = i + 1 < vr ? y1 : 0.f;
     }
     pk[i >> 1] = rf_pack2<kBf16>(y0, y1);
   }
@@ -174,17 +173,18 @@ __device__ __forceinline__ void store_row(uint32_t taddr, bool have, float f, bo
   }
 }
 
-// dQ.  A step is (key block, 64-key half); the two halves use two sets of TMEM
-// columns (S_1, S_2, dA: 64 each at [192 h, +192)), so one half's matrix
-// products run while the other half's dS is computed.  Warpgroup e computes map
-// e % 2 of half e / 2 (thread = query row = TMEM lane) and writes dS over the
-// first half of that map's S columns.  dQ accumulates at [384, 512): 64 columns
-// per map (at D = 64 both maps' columns of the product, half of them unused, so
-// that every operand starts at a box).
-// Issue order after dS of step t: dQ(t), dA(t + 2), then - once dQ(t) has read
-// the dS columns, by which time dA runs - S_1 and S_2 of t + 2.
-// Bound: per 128 x 128 block the ex2 unit 2,048 cycles; the tensor pipe about
-// 2,100 (N = 64 products are fed from shared memory at two thirds of its rate).
+// dQ.  A step is 64 keys of a listed block.  Two sets of TMEM columns (S_1, S_2,
+// dA: 64 each at [192 p, +192)) alternate, so that a step's products run while
+// the step before is computed.  Thread = query row = TMEM lane; warpgroup e takes
+// keys [16 e, +16) of the step, one 16-wide slice of the reduction of dQ, of both
+// maps, and writes dS_1 and dS_2 over S_1 and S_2 columns that it alone has read.
+// dQ accumulates at [384, 512): 64 columns per map (at D = 64 both maps' columns
+// of the product, half of them unused, so that every operand starts at a box).
+// A barrier check costs its warp 100 cycles and more: one barrier tells the
+// issuing warp that a step's tiles have landed and that its columns are free.
+// Bound: per 128 x 128 block the tensor pipe about 2,300 cycles (an N = 64
+// product with both operands in shared memory takes 54 cycles, 35 with A in
+// TMEM, 32 by its arithmetic); the ex2 unit 2,048.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     rf_diff_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -218,13 +218,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(rf_smem_u32(&sm.bar_q), 1);
     mbar_init(rf_smem_u32(&sm.bar_aux), 1);
     for (int i = 0; i < kQStages; ++i) {
-      mbar_init(rf_smem_u32(&sm.bar_full[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_full[i]), 2);
       mbar_init(rf_smem_u32(&sm.bar_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(rf_smem_u32(&sm.bar_sd_full[i]), 1);
-      mbar_init(rf_smem_u32(&sm.bar_ds_full[i]), 256);
-      mbar_init(rf_smem_u32(&sm.bar_dq_done[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_ds_full[i]), kCompute);
     }
     mbar_init(rf_smem_u32(&sm.bar_final), 1);
     mbar_init(rf_smem_u32(&sm.bar_drain), 1);
@@ -325,51 +324,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dv0 = umma_desc_sw128(rf_smem_u32(sm.v[0]), 16, 1024);
       const uint64_t dkn0 = umma_desc_sw128(rf_smem_u32(sm.k[0]), kHalfBox, 1024);
       const int nt = 2 * nv;
-      auto issue_da = [&](int t) {  // dA of step t
-        const int h = t & 1, st = t % kQStages;
-        const uint64_t dv = dv0 + (uint64_t)(st * (kTileBytes / 2) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t in = (kk & 3) * 32, box = kk >> 2;
-          mma_ss(tmem + 192 * h + 128, ddo + ((box * kBoxBytes + in) >> 4), dv + ((box * kHalfBox + in) >> 4), id_sd,
-                 kk > 0 ? 1u : 0u);
-        }
-      };
-      auto issue_s = [&](int t) {  // S_1 and S_2 of step t
-        const int h = t & 1;
-        const uint64_t dk = dk0 + (uint64_t)((t % kQStages) * (kTileBytes / 2) >> 4);
+      auto issue_sd = [&](int t) {  // S_1, S_2 and dA of step t
+        const uint32_t d = tmem + 192 * (t & 1);
+        const uint64_t st = (uint64_t)((t % kQStages) * (kTileBytes / 2) >> 4);
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk) {
             const uint32_t byte = w * D + kk * 32, box = byte >> 7, in = byte & 127;
-            mma_ss(tmem + 192 * h + 64 * w, dq + ((box * kBoxBytes + in) >> 4), dk + ((box * kHalfBox + in) >> 4), id_sd,
+            mma_ss(d + 64 * w, dq + ((box * kBoxBytes + in) >> 4), dk0 + st + ((box * kHalfBox + in) >> 4), id_sd,
                    kk > 0 ? 1u : 0u);
           }
-        tc_commit(rf_smem_u32(&sm.bar_sd_full[h]));
-      };
-      bool ok = warp_wait<true>(rf_smem_u32(&sm.bar_q), 0, abort);
-      for (int t = 0; ok && t < 2; ++t) {
-        ok = warp_wait<true>(rf_smem_u32(&sm.bar_full[t]), 0, abort);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_da(t);
-          issue_s(t);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t in = (kk & 3) * 32, box = kk >> 2;
+          mma_ss(d + 128, ddo + ((box * kBoxBytes + in) >> 4), dv0 + st + ((box * kHalfBox + in) >> 4), id_sd,
+                 kk > 0 ? 1u : 0u);
         }
+        tc_commit(rf_smem_u32(&sm.bar_sd_full[t & 1]));
+      };
+      // the first two steps' columns are free from the start
+      if (lane < 2) mbar_arrive(rf_smem_u32(&sm.bar_full[lane]));
+      __syncwarp();
+      bool ok = warp_wait<true>(rf_smem_u32(&sm.bar_q), 0, abort) &&
+                warp_wait<true>(rf_smem_u32(&sm.bar_full[0]), 0, abort);
+      if (ok) {
+        tc_fence_after();
+        if (elect_one()) issue_sd(0);
         __syncwarp();
       }
       for (int t = 0; ok && t < nt; ++t) {
         const int h = t & 1, st = t % kQStages;
-        const uint32_t ph = (t >> 1) & 1;  // each half's barriers complete once per block
-        // Every barrier check takes about as long as two MMAs: this one is made
-        // while dS is still being computed.
-        if (t + 2 < nt &&
-            !warp_wait<true>(rf_smem_u32(&sm.bar_full[(t + 2) % kQStages]), ((t + 2) / kQStages) & 1, abort)) {
-          ok = false;
-          break;
+        if (t + 1 < nt) {
+          if (!warp_wait<true>(rf_smem_u32(&sm.bar_full[(t + 1) % kQStages]), ((t + 1) / kQStages) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) issue_sd(t + 1);
+          __syncwarp();
         }
-        if (!warp_wait<true>(rf_smem_u32(&sm.bar_ds_full[h]), ph, abort)) { ok = false; break; }
+        if (!warp_wait<true>(rf_smem_u32(&sm.bar_ds_full[h]), (t >> 1) & 1, abort)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
           const uint64_t dk = dkn0 + (uint64_t)(st * (kTileBytes / 2) >> 4);
@@ -377,21 +372,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_ts(tmem + kDq + 64 * w, tmem + 192 * h + 64 * w + 8 * kk,
+              mma_ts(tmem + kDq + 64 * w, tmem + 192 * h + 64 * w + 16 * kk,
                      dk + (uint64_t)(((D == 128 ? w : 0) * kHalfBox + kk * 2048) >> 4), id_dq,
                      (t > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(rf_smem_u32(&sm.bar_dq_done[h]));
           tc_commit(rf_smem_u32(&sm.bar_empty[st]));
+          if (t + 2 < nt) tc_commit(rf_smem_u32(&sm.bar_full[(t + 2) % kQStages]));
         }
         __syncwarp();
-        if (t + 2 < nt) {
-          if (elect_one()) issue_da(t + 2);
-          __syncwarp();
-          if (!warp_wait<true>(rf_smem_u32(&sm.bar_dq_done[h]), ph, abort)) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) issue_s(t + 2);
-          __syncwarp();
-        }
       }
       if (!ok && lane == 0) record_timeout(abort, a.status, 6);
       if (elect_one()) {
@@ -404,40 +391,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------- dS and epilogue ----------------
-    const int e = warp >> 2, w = e & 1, h = e >> 1;
+    const int e = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t scol = lane_base + 192 * h + 64 * w, acol = lane_base + 192 * h + 128;
-    const float* st = a.stats + ((size_t)n * g.t_qblk + tb) * (4 * RF_BLOCK);
-    const float* str = st + (r >> 6) * 256 + (r & 63);
-    const float nlse = str[w * 64];
-    const float c = (w == 0 ? 1.f : -a.lambda[n]) * (kBf16 ? 1.f : rf_pow2(es));
-    const float dc = c * str[(2 + w) * 64];
+    const float* str = a.stats + ((size_t)n * g.t_qblk + tb) * (4 * RF_BLOCK) + (r >> 6) * 256 + (r & 63);
+    const float c1 = kBf16 ? 1.f : rf_pow2(es), c2 = -a.lambda[n] * c1;
+    const float nlse1 = str[0], nlse2 = str[64], dc1 = c1 * str[128], dc2 = c2 * str[192];
     bool ok = true;
-    for (int b = 0; b < nv; ++b) {
-      if (!warp_wait(rf_smem_u32(&sm.bar_sd_full[h]), b & 1, abort)) { ok = false; break; }
+    for (int t = 0; t < 2 * nv; ++t) {
+      if (!warp_wait(rf_smem_u32(&sm.bar_sd_full[t & 1]), (t >> 1) & 1, abort)) { ok = false; break; }
       tc_fence_after();
-      const int vr = (sm.list[b] == s.n_pb - 1) ? vr_last : RF_BLOCK;
-      uint32_t sr[2][16], da[2][16];
-      tmem_ld16(scol, sr[0]);
-      tmem_ld16(acol, da[0]);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        tmem_wait_ld();
-        tmem_pin16(sr[x & 1]);
-        tmem_pin16(da[x & 1]);
-        if (x < 3) {  // the next 16 columns, on their way while these are computed
-          tmem_ld16(scol + 16 * (x + 1), sr[(x + 1) & 1]);
-          tmem_ld16(acol + 16 * (x + 1), da[(x + 1) & 1]);
-        }
-        uint32_t pk[8];
-        if (vr == RF_BLOCK) ds_chunk<kBf16, true>(sr[x & 1], da[x & 1], 64 * h + 16 * x, vr, a.sl2, nlse, c, dc, pk);
-        else                ds_chunk<kBf16, false>(sr[x & 1], da[x & 1], 64 * h + 16 * x, vr, a.sl2, nlse, c, dc, pk);
-        tmem_st8(scol + 8 * x, pk);
-      }
+      const uint32_t base = lane_base + 192 * (t & 1) + 16 * e;
+      // valid keys of this thread's 16 (all of them but in the partial prefix block)
+      const int vr = (sm.list[t >> 1] == s.n_pb - 1 ? vr_last : RF_BLOCK) - 64 * (t & 1) - 16 * e;
+      uint32_t s1[16], s2[16], da[16], pk[8];
+      tmem_ld16(base, s1);
+      tmem_ld16(base + 64, s2);
+      tmem_ld16(base + 128, da);
+      tmem_wait_ld();
+      tmem_pin16(s1);
+      tmem_pin16(s2);
+      tmem_pin16(da);
+      if (vr >= 16) ds_chunk<kBf16, true>(s1, da, vr, a.sl2, nlse1, c1, dc1, pk);
+      else          ds_chunk<kBf16, false>(s1, da, vr, a.sl2, nlse1, c1, dc1, pk);
+      tmem_st8(base, pk);
+      if (vr >= 16) ds_chunk<kBf16, true>(s2, da, vr, a.sl2, nlse2, c2, dc2, pk);
+      else          ds_chunk<kBf16, false>(s2, da, vr, a.sl2, nlse2, c2, dc2, pk);
+      tmem_st8(base + 64, pk);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(rf_smem_u32(&sm.bar_ds_full[h]));
+      mbar_arrive(rf_smem_u32(&sm.bar_ds_full[t & 1]));
     }
     if (!ok) record_timeout(abort, a.status, 7);
     const bool have = nv > 0 && !*abort && warp_wait(rf_smem_u32(&sm.bar_final), 0, abort) && !*abort;
@@ -462,14 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // query rows of one (head, query block) that lists the block: S_w^T and dA^T
 // with N = 64, A^T, dS_w^T from registers, then dV += A^T dO, dK_w += dS_w^T Q_w.
 // TMEM: dV at [256, 256 + D), dK at [384, 512) (per map 64 columns, as dQ), and
-// four 64-column slots in which a step's S_1, S_2 and dA take turns.  S_1 of the
-// next step goes into the free slot; its S_2 and dA into dA's and S_1's as soon as
-// this step's numbers are in registers, long before they are used up; dS_1 and
-// dS_2 are written over S_2, each thread over columns that it alone has read, and
-// A^T goes through shared memory (two buffers).  So the elements of a step never
-// wait for its matrix products, and the warpgroups drift apart until one's
-// exponentials run under another's arithmetic.  A barrier check costs its warp
-// 100 to 200 cycles; the two that a step makes are what is left of five.
+// four 64-column slots in which a step's S_1, S_2 and dA take turns: the next
+// step's go into the free slot and into dA's and S_1's as soon as this step's
+// numbers are in registers, long before they are used up; dS_1 and dS_2 are
+// written over S_2, each thread over columns that it alone has read, and A^T goes
+// through shared memory (two buffers).  So a step's elements hardly ever wait for
+// its products, and the warpgroups drift apart until one's exponentials run under
+// another's arithmetic.  A barrier check costs its warp 100 to 200 cycles, so
+// there are few: one per step for a computing thread, three for the issuing warp.
 // Warpgroup e takes queries [16 e, +16) of the step, which is one 16-wide slice
 // of the reduction of dV and dK.
 // Rows that a query block does not have carry -lse = -inf (P = 0); their Q and
@@ -508,15 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(rf_smem_u32(&sm.bar_kv), 1);
     mbar_init(rf_smem_u32(&sm.bar_aux), 1);
     for (int i = 0; i < kKvStages; ++i) {
-      mbar_init(rf_smem_u32(&sm.bar_full[i]), 1);
+      mbar_init(rf_smem_u32(&sm.bar_full[i]), 2);
       mbar_init(rf_smem_u32(&sm.bar_empty[i]), 1);
     }
-    mbar_init(rf_smem_u32(&sm.bar_s1_full[0]), 2);  // the product's commit, and the issuing warp itself
-    mbar_init(rf_smem_u32(&sm.bar_s1_full[1]), 2);
-    mbar_init(rf_smem_u32(&sm.bar_da_full), 1);
+    mbar_init(rf_smem_u32(&sm.bar_sd_full), 2);  // the products' commit, and the issuing warp itself
     mbar_init(rf_smem_u32(&sm.bar_read), kCompute);
-    mbar_init(rf_smem_u32(&sm.bar_ew), kCompute);
-    mbar_init(rf_smem_u32(&sm.bar_y_done), 1);
+    mbar_init(rf_smem_u32(&sm.bar_ew[0]), kCompute);
+    mbar_init(rf_smem_u32(&sm.bar_ew[1]), kCompute);
     mbar_init(rf_smem_u32(&sm.bar_final), 1);
     mbar_init(rf_smem_u32(&sm.bar_drain), 1);
     sm.abort = 0;
@@ -632,69 +613,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t don0 = umma_desc_sw128(rf_smem_u32(sm.d_o[0]), kHalfBox, 1024);
       const uint64_t da_t = umma_desc_sw128(rf_smem_u32(sm.a[0]), 16, 1024);
       const int nt = 2 * ni;
-      // slots of step t: S_1, S_2, dA (the fourth is free for the next S_1)
+      // slots of step t: S_1, S_2, dA (the fourth takes the next S_1)
       auto slot = [&](int t, int which) -> uint32_t {
         const uint32_t tab = which == 0 ? 0x2130u : (which == 1 ? 0x3021u : 0x1302u);
         return tmem + 64u * ((tab >> (4 * (t & 3))) & 15u);
       };
       auto tile_off = [&](int t) -> uint64_t { return (uint64_t)((t % kKvStages) * (kTileBytes / 2) >> 4); };
-      auto issue_s = [&](int t, int w) {
-        const uint64_t b = dq0 + tile_off(t);
+      auto issue_sd = [&](int t) {  // S_1, S_2 and dA of step t
 #pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk) {
-          const uint32_t byte = w * D + kk * 32, box = byte >> 7, in = byte & 127;
-          mma_ss(slot(t, w), dk + ((box * kBoxBytes + in) >> 4), b + ((box * kHalfBox + in) >> 4), id_s, kk > 0 ? 1u : 0u);
+        for (int w = 0; w < 2; ++w) {
+          const uint64_t b = dq0 + tile_off(t);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) {
+            const uint32_t byte = w * D + kk * 32, box = byte >> 7, in = byte & 127;
+            mma_ss(slot(t, w), dk + ((box * kBoxBytes + in) >> 4), b + ((box * kHalfBox + in) >> 4), id_s,
+                   kk > 0 ? 1u : 0u);
+          }
         }
-        if (w == 0) {
-          // The arrival hands on what this thread has seen: the step's tiles and
-          // numbers in shared memory, and A's buffer read (bar_y_done of t - 2).
-          mbar_arrive(rf_smem_u32(&sm.bar_s1_full[t & 1]));
-          tc_commit(rf_smem_u32(&sm.bar_s1_full[t & 1]));
-        }
-      };
-      auto issue_da = [&](int t) {
         const uint64_t b = do0 + tile_off(t);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t in = (kk & 3) * 32, box = kk >> 2;
           mma_ss(slot(t, 2), dv + ((box * kBoxBytes + in) >> 4), b + ((box * kHalfBox + in) >> 4), id_s, kk > 0 ? 1u : 0u);
         }
-        tc_commit(rf_smem_u32(&sm.bar_da_full));
+        // The arrival hands on what this thread has seen: the step's numbers in
+        // shared memory, and A's buffer read.
+        mbar_arrive(rf_smem_u32(&sm.bar_sd_full));
+        tc_commit(rf_smem_u32(&sm.bar_sd_full));
       };
+      // the first two steps' buffer and slot are free from the start
+      if (lane < 2) mbar_arrive(rf_smem_u32(&sm.bar_full[lane]));
+      __syncwarp();
       bool ok = warp_wait<true>(rf_smem_u32(&sm.bar_kv), 0, abort) &&
                 warp_wait<true>(rf_smem_u32(&sm.bar_full[0]), 0, abort);
       if (ok) {
         tc_fence_after();
-        if (elect_one()) {
-          issue_s(0, 0);
-          issue_s(0, 1);
-          issue_da(0);
-        }
+        if (elect_one()) issue_sd(0);
         __syncwarp();
       }
       for (int t = 0; ok && t < nt; ++t) {
-        const bool more = t + 1 < nt;
-        if (more) {
-          if (!warp_wait<true>(rf_smem_u32(&sm.bar_full[(t + 1) % kKvStages]), ((t + 1) / kKvStages) & 1, abort)) {
+        if (t + 1 < nt) {
+          if (!warp_wait<true>(rf_smem_u32(&sm.bar_full[(t + 1) % kKvStages]), ((t + 1) / kKvStages) & 1, abort) ||
+              !warp_wait<true>(rf_smem_u32(&sm.bar_read), t & 1, abort)) {
             ok = false;
             break;
           }
-          // the slot of S_1(t + 1) held dS_1(t - 1) and dS_2(t - 1)
-          if (t > 0 && !warp_wait<true>(rf_smem_u32(&sm.bar_y_done), (t - 1) & 1, abort)) { ok = false; break; }
           tc_fence_after();
-          if (elect_one()) issue_s(t + 1, 0);
+          if (elect_one()) issue_sd(t + 1);
           __syncwarp();
         }
-        if (more) {
-          if (!warp_wait<true>(rf_smem_u32(&sm.bar_read), t & 1, abort)) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) {
-            issue_s(t + 1, 1);
-            issue_da(t + 1);
-          }
-          __syncwarp();
-        }
-        if (!warp_wait<true>(rf_smem_u32(&sm.bar_ew), t & 1, abort)) { ok = false; break; }
+        if (!warp_wait<true>(rf_smem_u32(&sm.bar_ew[t & 1]), (t >> 1) & 1, abort)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
           const uint64_t bo = don0 + tile_off(t), bq = dqn0 + tile_off(t);
@@ -702,15 +670,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t acc = t > 0 ? 1u : 0u;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss(tmem + kDv, da_t + (uint64_t)(((t & 1) * (RF_BLOCK * 128) + kk * 32) >> 4), bo + (uint64_t)(kk * 2048 >> 4), id_dv, kk > 0 ? 1u : acc);
+            mma_ss(tmem + kDv, da_t + (uint64_t)(((t & 1) * (RF_BLOCK * 128) + kk * 32) >> 4),
+                   bo + (uint64_t)(kk * 2048 >> 4), id_dv, kk > 0 ? 1u : acc);
 #pragma unroll
           for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_ts(tmem + kDk + 64 * w, sb + 16 * kk + 8 * (1 - w),
                      bq + (uint64_t)(((D == 128 ? w : 0) * kHalfBox + kk * 2048) >> 4), id_dk, kk > 0 ? 1u : acc);
-          tc_commit(rf_smem_u32(&sm.bar_y_done));
           tc_commit(rf_smem_u32(&sm.bar_empty[t % kKvStages]));
+          if (t + 2 < nt) tc_commit(rf_smem_u32(&sm.bar_full[(t + 2) % kKvStages]));
         }
         __syncwarp();
       }
@@ -746,12 +715,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int st = t % kKvStages;
       // this thread's 16 queries' numbers: -lse_1, -lse_2, delta_1, delta_2, 256 bytes apart
       const uint32_t num = stats0 + (uint32_t)st * kStatBytes;
-      if (!warp_wait(rf_smem_u32(&sm.bar_s1_full[t & 1]), (t >> 1) & 1, abort)) { ok = false; break; }
+      if (!warp_wait(rf_smem_u32(&sm.bar_sd_full), t & 1, abort)) { ok = false; break; }
       tc_fence_after();
-      uint32_t s1[16], s2[16];
+      uint32_t s1[16], s2[16], da[16];
       tmem_ld16(s1c, s1);
+      tmem_ld16(s2c, s2);
+      tmem_ld16(dac, da);
       tmem_wait_ld();
       tmem_pin16(s1);
+      tmem_pin16(s2);
+      tmem_pin16(da);
+      tc_fence_before();
+      mbar_arrive(rf_smem_u32(&sm.bar_read));
       auto exps = [&](uint32_t* x, uint32_t nl) {
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
@@ -771,17 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           x[i + 3] = __float_as_uint(rf_ex2(f3));
         }
       };
-      exps(s1, num);  // P_1, while S_2 and dA are still being computed
-      if (!warp_wait(rf_smem_u32(&sm.bar_da_full), t & 1, abort)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t da[16];
-      tmem_ld16(s2c, s2);
-      tmem_ld16(dac, da);
-      tmem_wait_ld();
-      tmem_pin16(s2);
-      tmem_pin16(da);
-      tc_fence_before();
-      mbar_arrive(rf_smem_u32(&sm.bar_read));
+      exps(s1, num);
       exps(s2, num + 256);
       const float nlam = -lds_f(rf_smem_u32(&sm.lam[0]) + 4u * st);
       const uint64_t nl2 = rf_f2(__float_as_uint(nlam), __float_as_uint(nlam));
@@ -823,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st16(s2c, out);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(rf_smem_u32(&sm.bar_ew));
+      mbar_arrive(rf_smem_u32(&sm.bar_ew[t & 1]));
     }
     if (!ok) record_timeout(abort, a.status, 10);
     const bool have = ni > 0 && !*abort && warp_wait(rf_smem_u32(&sm.bar_final), 0, abort) && !*abort;
