@@ -27,6 +27,7 @@
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kReduceThreads = 1024;  // small sums over many slices: latency, so many in flight
 constexpr int kMaxRowWidth = 1024;  // widest group held in one warp's registers
 
 struct NormArgs {
@@ -63,32 +64,88 @@ template <> __device__ __forceinline__ float from_f<float>(float v) { return v; 
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
-// VEC elements (16 bytes when VEC > 1) to and from fp32.
+// VEC elements (16 bytes when VEC > 1) as they lie in memory, and to and from fp32.
+template <class T, int VEC> struct RawVec { using type = uint4; };
+template <class T> struct RawVec<T, 1> { using type = T; };
+__device__ __forceinline__ void unpack_word(uint32_t w, float* f, float) { f[0] = __uint_as_float(w); }
+__device__ __forceinline__ void unpack_word(uint32_t w, float* f, __nv_bfloat16) {
+  f[0] = __uint_as_float(w << 16);
+  f[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void unpack_word(uint32_t w, float* f, __half) {
+  f[0] = __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)));
+  f[1] = __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+}
+template <class T, int VEC>
+__device__ __forceinline__ void unpack_v(const typename RawVec<T, VEC>::type& u, float* f) {
+  if constexpr (VEC == 1) {
+    f[0] = to_f(u);
+  } else {
+    constexpr int kPer = VEC / 4;
+    unpack_word(u.x, f, T{});
+    unpack_word(u.y, f + kPer, T{});
+    unpack_word(u.z, f + 2 * kPer, T{});
+    unpack_word(u.w, f + 3 * kPer, T{});
+  }
+}
+__device__ __forceinline__ uint32_t pack_word(const float* f, float) { return __float_as_uint(f[0]); }
+__device__ __forceinline__ uint32_t pack_word(const float* f, __nv_bfloat16) { return rf_pack2<true>(f[0], f[1]); }
+__device__ __forceinline__ uint32_t pack_word(const float* f, __half) { return rf_pack2<false>(f[0], f[1]); }
 template <class T, int VEC>
 __device__ __forceinline__ void load_v(const T* p, float* f) {
-  if constexpr (VEC == 1) {
-    f[0] = to_f(*p);
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const T* t = reinterpret_cast<const T*>(&u);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = to_f(t[i]);
-  }
+  using Raw = typename RawVec<T, VEC>::type;
+  unpack_v<T, VEC>(*reinterpret_cast<const Raw*>(p), f);
 }
 template <class T, int VEC>
 __device__ __forceinline__ void store_v(T* p, const float* f) {
   if constexpr (VEC == 1) {
     *p = from_f<T>(f[0]);
   } else {
-    uint4 u;
-    T* t = reinterpret_cast<T*>(&u);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) t[i] = from_f<T>(f[i]);
-    *reinterpret_cast<uint4*>(p) = u;
+    constexpr int kPer = VEC / 4;
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_word(f, T{}), pack_word(f + kPer, T{}), pack_word(f + 2 * kPer, T{}),
+                                              pack_word(f + 3 * kPer, T{}));
   }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+// gamma or beta of VEC channels from channel i on; vector loads where they are aligned.
+template <int VEC>
+__device__ __forceinline__ void load_pv(const void* p, int dt, long long i, float* f) {
+  if (VEC > 1 && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && i % VEC == 0) {
+    if (dt == RF_FP32) {
+#pragma unroll
+      for (int k = 0; k + 4 <= VEC; k += 4) load_v<float, 4>(static_cast<const float*>(p) + i + k, f + k);
+      return;
+    }
+    if constexpr (VEC == 8) {
+      if (dt == RF_BF16) load_v<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16*>(p) + i, f);
+      else               load_v<__half, 8>(static_cast<const __half*>(p) + i, f);
+      return;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) f[k] = load_p(p, dt, i + k);
+}
+// {mean, 1 / sqrt} (or the backward pass's two means) of the groups of VEC channels.
+template <int VEC>
+__device__ __forceinline__ void load_stats(const float* st, long long first_group, int c, int width, float* m, float* r) {
+  if (width % VEC == 0) {  // one group
+    const float2 s = *reinterpret_cast<const float2*>(st + 2 * (first_group + c / width));
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      m[k] = s.x;
+      r[k] = s.y;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      const float2 s = *reinterpret_cast<const float2*>(st + 2 * (first_group + (c + k) / width));
+      m[k] = s.x;
+      r[k] = s.y;
+    }
+  }
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 __device__ __forceinline__ float act_f(float z, int act) { return act == RF_ACT_SILU ? z * sigmoid(z) : z; }
 // derivative of the activation at z
 __device__ __forceinline__ float act_d(float z, int act) {
@@ -99,110 +156,123 @@ __device__ __forceinline__ float act_d(float z, int act) {
 
 // Sum over the `lanes` (a power of two) neighbouring lanes of a sub-warp.
 __device__ __forceinline__ float sub_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
 // One row at a time per sub-warp of `lanes` lanes, NV vectors of VEC channels per
-// lane, kRows rows loaded before the first is used; blockIdx.y = group, so that
-// gamma, beta and (backward) the channels' sums stay in registers over all rows
-// of the CTA's slice.
+// lane; blockIdx.y = group, so that gamma, beta and (backward) the channels' sums
+// stay in registers over all rows of the CTA's slice.  kPre rows are on their
+// way from memory, unconverted, while one is computed.
 template <class T, int VEC, int NV, bool kBwd>
-__global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? 4 : 1) rf_norm_row_kernel(const __grid_constant__ NormArgs a, int lanes) {
+__global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? (kBwd ? 2 : 4) : 1)
+    rf_norm_row_kernel(const __grid_constant__ NormArgs a, int lanes) {
   constexpr int E = VEC * NV;
-  constexpr int kRows = E <= 8 ? (kBwd ? 2 : 4) : 1;
+  constexpr int kPre = E <= 8 ? 2 : 1;
+  using Raw = typename RawVec<T, VEC>::type;
   const int g = blockIdx.y, lane = threadIdx.x % lanes, sub = threadIdx.x / lanes, subs = kThreads / lanes;
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
-  T* y = static_cast<T*>(a.y);
+  const T* x = static_cast<const T*>(a.x) + g * a.xs_g + lane * VEC;
+  const T* dy = static_cast<const T*>(a.dy) + g * a.ys_g + lane * VEC;
+  T* out = static_cast<T*>(a.y) + (kBwd ? g * a.xs_g : g * a.ys_g) + lane * VEC;
   float gm[E], bt[E], sg[kBwd ? E : 1], sb[kBwd ? E : 1];
-  bool have[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = (v * lanes + lane) * VEC;
-    have[v] = c < a.width;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      gm[v * VEC + i] = have[v] ? load_p(a.gamma, a.pdt, (long long)g * a.width + c + i) : 0.f;
-      bt[v * VEC + i] = have[v] ? load_p(a.beta, a.pdt, (long long)g * a.width + c + i) : 0.f;
+      gm[v * VEC + i] = c < a.width ? load_p(a.gamma, a.pdt, (long long)g * a.width + c + i) : 0.f;
+      bt[v * VEC + i] = c < a.width ? load_p(a.beta, a.pdt, (long long)g * a.width + c + i) : 0.f;
       if constexpr (kBwd) sg[v * VEC + i] = sb[v * VEC + i] = 0.f;
     }
   }
+  const int mine = (a.width / VEC - lane + lanes - 1) / lanes;  // vectors of this lane (v < mine)
   const float inv = 1.0f / (float)a.width;
   const long long per = (a.n_rows + a.slices - 1) / a.slices;
   const long long first = (long long)blockIdx.x * per, last = min(a.n_rows, first + per);
-  // batch element and row of this sub-warp's next row, carried along
-  long long b = (first + sub) / a.rows, r = (first + sub) - b * a.rows;
-  // every lane of a warp runs the same number of turns (the sums use the whole warp)
-  for (long long base = first; base < last; base += (long long)subs * kRows) {
-    float xv[kRows][E], dv[kBwd ? kRows : 1][kBwd ? E : 1];
-    long long xo[kRows], yo[kRows];
-    bool live[kRows];
+  const int n_mine = last > first ? (int)(last - first) : 0;  // at most 2^30: check_desc
+  const int count = (n_mine + subs - 1) / subs;
+  // batch element and row of the next row to load, and of the row to store
+  const int n_r = (int)a.rows;
+  int lb = (int)((first + sub) / a.rows), lr = (int)((first + sub) - lb * a.rows), sb_ = lb, sr = lr;
+  Raw xr[kPre][NV], dr[kBwd ? kPre : 1][kBwd ? NV : 1];
+  auto load = [&](int i, int slot) {
+    const bool live = sub + i * subs < n_mine;
+    const T* px = x + (lb * a.xs_b + lr * a.xs_r);
+    const T* pd = dy + (kBwd ? lb * a.ys_b + lr * a.ys_r : 0);
 #pragma unroll
-    for (int w = 0; w < kRows; ++w) {
-      live[w] = base + sub + (long long)w * subs < last;
-      xo[w] = b * a.xs_b + r * a.xs_r + g * a.xs_g;
-      yo[w] = b * a.ys_b + r * a.ys_r + g * a.ys_g;
-      r += subs;
-      while (r >= a.rows) {
-        r -= a.rows;
-        ++b;
-      }
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        if (have[v] && live[w]) {
-          load_v<T, VEC>(x + xo[w] + (v * lanes + lane) * VEC, xv[w] + v * VEC);
-          if constexpr (kBwd) load_v<T, VEC>(dy + yo[w] + (v * lanes + lane) * VEC, dv[w] + v * VEC);
-        } else {
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            xv[w][v * VEC + k] = 0.f;
-            if constexpr (kBwd) dv[w][v * VEC + k] = 0.f;
-          }
-        }
+    for (int v = 0; v < NV; ++v) {
+      xr[slot][v] = Raw{};
+      if constexpr (kBwd) dr[slot][v] = Raw{};
+      if (live && v < mine) {
+        xr[slot][v] = *reinterpret_cast<const Raw*>(px + v * lanes * VEC);
+        if constexpr (kBwd) dr[slot][v] = *reinterpret_cast<const Raw*>(pd + v * lanes * VEC);
       }
     }
+    lr += subs;
+    while (lr >= n_r) {
+      lr -= n_r;
+      ++lb;
+    }
+  };
 #pragma unroll
-    for (int w = 0; w < kRows; ++w) {
+  for (int i = 0; i < kPre; ++i) load(i, i);
+  // every lane of a warp runs the same number of turns (the sums use the whole warp)
+  for (int i0 = 0; i0 < count; i0 += kPre) {
+#pragma unroll
+    for (int w = 0; w < kPre; ++w) {
+      const int i = i0 + w;
+      const bool live = sub + i * subs < n_mine;
+      float xv[E], dv[kBwd ? E : 1];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        unpack_v<T, VEC>(xr[w][v], xv + v * VEC);
+        if constexpr (kBwd) unpack_v<T, VEC>(dr[w][v], dv + v * VEC);
+      }
+      load(i + kPre, w);
       float s = 0.f;
 #pragma unroll
-      for (int k = 0; k < E; ++k) s += xv[w][k];
+      for (int k = 0; k < E; ++k) s += xv[k];
       const float mu = sub_sum(s, lanes) * inv;
       s = 0.f;
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int k = v * VEC; k < (v + 1) * VEC; ++k) {
-          xv[w][k] = have[v] ? xv[w][k] - mu : 0.f;
-          s = fmaf(xv[w][k], xv[w][k], s);
-        }
+      for (int k = 0; k < E; ++k) {
+        xv[k] = k / VEC < mine ? xv[k] - mu : 0.f;
+        s = fmaf(xv[k], xv[k], s);
+      }
       const float rstd = rsqrtf(sub_sum(s, lanes) * inv + a.eps);
       if constexpr (!kBwd) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) xv[w][k] = act_f(fmaf(xv[w][k] * rstd, gm[k], bt[k]), a.act);
+        for (int k = 0; k < E; ++k) xv[k] = act_f(fmaf(xv[k] * rstd, gm[k], bt[k]), a.act);
       } else {
         float m1 = 0.f, m2 = 0.f;
 #pragma unroll
         for (int k = 0; k < E; ++k) {
-          xv[w][k] *= rstd;
+          xv[k] *= rstd;
           // a row past the end has dy = 0, and so g = 0, unless eps = 0 makes its xh NaN
-          const float gz = live[w] ? dv[w][k] * act_d(fmaf(xv[w][k], gm[k], bt[k]), a.act) : 0.f;
-          sg[k] = live[w] ? fmaf(gz, xv[w][k], sg[k]) : sg[k];
+          const float gz = live ? dv[k] * act_d(fmaf(xv[k], gm[k], bt[k]), a.act) : 0.f;
+          sg[k] = live ? fmaf(gz, xv[k], sg[k]) : sg[k];
           sb[k] += gz;
-          dv[w][k] = gz * gm[k];
-          m1 += dv[w][k];
-          m2 = fmaf(dv[w][k], xv[w][k], m2);
+          dv[k] = gz * gm[k];
+          m1 += dv[k];
+          m2 = fmaf(dv[k], xv[k], m2);
         }
         m1 = sub_sum(m1, lanes) * inv;
         m2 = sub_sum(m2, lanes) * inv;
 #pragma unroll
-        for (int k = 0; k < E; ++k) xv[w][k] = rstd * (dv[w][k] - m1 - xv[w][k] * m2);
+        for (int k = 0; k < E; ++k) xv[k] = rstd * (dv[k] - m1 - xv[k] * m2);
       }
-      if (live[w]) {
-        const long long oo = kBwd ? xo[w] : yo[w];
+      if (live) {
+        T* po = out + (kBwd ? sb_ * a.xs_b + sr * a.xs_r : sb_ * a.ys_b + sr * a.ys_r);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-          if (have[v]) store_v<T, VEC>(y + oo + (v * lanes + lane) * VEC, xv[w] + v * VEC);
+          if (v < mine) store_v<T, VEC>(po + v * lanes * VEC, xv + v * VEC);
+      }
+      sr += subs;
+      while (sr >= n_r) {
+        sr -= n_r;
+        ++sb_;
       }
     }
   }
@@ -213,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? 4 : 1) rf_norm_row_k
       if (sub == turn) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-          if (have[v])
+          if (v < mine)
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
               const int c = (v * lanes + lane) * VEC + k;
@@ -264,14 +334,9 @@ __global__ void __launch_bounds__(kThreads) rf_norm_partial_kernel(const __grid_
     if constexpr (!kBwd) {
       load_v<T, VEC>(x + (first + rl) * a.xs_r, x0);
     } else {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const int g = (int)(c + k) / a.width;
-        gm[k] = load_p(a.gamma, a.pdt, c + k);
-        bt[k] = load_p(a.beta, a.pdt, c + k);
-        mu[k] = a.stats[2 * (b * (long long)a.groups + g)];
-        rs[k] = a.stats[2 * (b * (long long)a.groups + g) + 1];
-      }
+      load_pv<VEC>(a.gamma, a.pdt, c, gm);
+      load_pv<VEC>(a.beta, a.pdt, c, bt);
+      load_stats<VEC>(a.stats, b * (long long)a.groups, (int)c, a.width, mu, rs);
     }
     const T* dy = static_cast<const T*>(a.dy) + (kBwd ? b * a.ys_b + chan_off(c, a.width, a.ys_g) : 0);
 #pragma unroll 8
@@ -349,105 +414,85 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.f;
+  float s = red[threadIdx.x & 31];
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) s += red[i];
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 
 // Forward: a (batch, group)'s mean and 1 / sqrt(var + eps) from its channels'
 // slices, about one of the slices' means (so that what cancels in the variance
 // is only how far the channels' means lie apart, which is part of it).
-__global__ void __launch_bounds__(kThreads) rf_norm_stats_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float red[kThreads / 32];
+// Backward: {mean(gamma g), mean(gamma g xh)}, behind the slices' sums in the
+// workspace.
+template <bool kBwd>
+__global__ void __launch_bounds__(kReduceThreads) rf_norm_stats_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float red[kReduceThreads / 32];
   const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
   const long long ch = (long long)a.groups * a.width;
   const float* w = a.ws + (long long)b * a.slices * 2 * ch + (long long)g * a.width;
   const int per = (int)((a.rows + a.slices - 1) / a.slices);
   const float inv = 1.0f / ((float)a.rows * (float)a.width);
-  const float ref = w[0];
+  const float ref = kBwd ? 0.f : w[0];
   float s = 0.f, q = 0.f;
-  const int stride = kThreads / min(a.width, kThreads);  // slices in parallel
-  const int c0 = threadIdx.x % min(a.width, kThreads), s0 = threadIdx.x / min(a.width, kThreads);
+  const int wide = min(a.width, kReduceThreads), stride = kReduceThreads / wide;  // channels, slices in parallel
+  const int c0 = threadIdx.x % wide, s0 = threadIdx.x / wide;
   if (s0 < stride)
-    for (int c = c0; c < a.width; c += kThreads)
-#pragma unroll 8
+    for (int c = c0; c < a.width; c += kReduceThreads) {
+      const float gm = kBwd ? load_p(a.gamma, a.pdt, (long long)g * a.width + c) : 0.f;
+#pragma unroll 4
       for (int sl = s0; sl < a.slices; sl += stride) {
-        const long long left = a.rows - (long long)sl * per;
-        if (left > 0) {
-          const float n = (float)min(left, (long long)per);
-          const float d = w[sl * 2 * ch + c] - ref, m2 = w[sl * 2 * ch + ch + c];
+        const float v0 = w[sl * 2 * ch + c], v1 = w[sl * 2 * ch + ch + c];
+        if constexpr (kBwd) {
+          s = fmaf(gm, v0, s);
+          q = fmaf(gm, v1, q);
+        } else {
+          // an empty slice's zeros count for nothing
+          const float n = (float)max(0, min((int)a.rows - sl * per, per)), d = v0 - ref;
           s = fmaf(n, d, s);
-          q += fmaf(n * d, d, m2);
+          q += fmaf(n * d, d, v1);
         }
       }
+    }
   s = block_sum(s, red) * inv;
   q = block_sum(q, red) * inv;
   if (threadIdx.x == 0) {
-    a.stats[2 * blockIdx.x] = ref + s;
-    a.stats[2 * blockIdx.x + 1] = rsqrtf(fmaxf(q - s * s, 0.f) + a.eps);
+    float* o = kBwd ? a.ws + (long long)a.batch * a.slices * 2 * ch : a.stats;
+    o[2 * blockIdx.x] = kBwd ? s : ref + s;
+    o[2 * blockIdx.x + 1] = kBwd ? q : rsqrtf(fmaxf(q - s * s, 0.f) + a.eps);
   }
 }
 
-// Backward: {mean(gamma g), mean(gamma g xh)} of a (batch, group), behind the
-// slices' sums in the workspace.
-__global__ void __launch_bounds__(kThreads) rf_norm_means_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float red[kThreads / 32];
-  const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
-  const long long ch = (long long)a.groups * a.width;
-  const float* w = a.ws + (long long)b * a.slices * 2 * ch + (long long)g * a.width;
-  const float inv = 1.0f / ((float)a.rows * (float)a.width);
-  float s0 = 0.f, s1 = 0.f;
-  const int stride = kThreads / min(a.width, kThreads);
-  const int c0 = threadIdx.x % min(a.width, kThreads), l0 = threadIdx.x / min(a.width, kThreads);
-  if (l0 < stride)
-    for (int c = c0; c < a.width; c += kThreads) {
-      float t0 = 0.f, t1 = 0.f;
-#pragma unroll 8
-      for (int sl = l0; sl < a.slices; sl += stride) {
-        t0 += w[sl * 2 * ch + c];
-        t1 += w[sl * 2 * ch + ch + c];
-      }
-      const float gm = load_p(a.gamma, a.pdt, (long long)g * a.width + c);
-      s0 = fmaf(gm, t0, s0);
-      s1 = fmaf(gm, t1, s1);
-    }
-  s0 = block_sum(s0, red);
-  s1 = block_sum(s1, red);
-  if (threadIdx.x == 0) {
-    float* m = a.ws + (long long)a.batch * a.slices * 2 * ch + 2 * blockIdx.x;
-    m[0] = s0 * inv;
-    m[1] = s1 * inv;
-  }
-}
-
-// dgamma and dbeta: the partial sums [parts][2][channels] added in order.
-// kGammaFirst: the first of the two is dgamma's.
-__global__ void __launch_bounds__(kThreads) rf_norm_params_kernel(const float* __restrict__ ws, long long parts,
-                                                                  long long ch, int gamma_first, int pdt,
-                                                                  void* dgamma, void* dbeta) {
-  // 32 channels per block, 8 lanes of parts, merged in order
-  __shared__ float red[2][8][32];
+// dgamma and dbeta: the partial sums [parts][2][channels] added in a fixed order.
+__global__ void __launch_bounds__(kReduceThreads) rf_norm_params_kernel(const float* __restrict__ ws, int parts,
+                                                                        long long ch, int gamma_first, int pdt,
+                                                                        void* dgamma, void* dbeta) {
+  // 32 channels per block, 32 lanes of parts, merged in order
+  __shared__ float red[2][32][33];
   const int cl = threadIdx.x & 31, pl = threadIdx.x >> 5;
   const long long c = (long long)blockIdx.x * 32 + cl;
   float s0 = 0.f, s1 = 0.f;
   if (c < ch)
-#pragma unroll 8
-    for (long long p = pl; p < parts; p += 8) {
+#pragma unroll 4
+    for (int p = pl; p < parts; p += 32) {
       s0 += ws[p * 2 * ch + c];
       s1 += ws[p * 2 * ch + ch + c];
     }
   red[0][pl][cl] = s0;
   red[1][pl][cl] = s1;
   __syncthreads();
-  if (pl == 0 && c < ch) {
+  // warp pl sums channel pl's 32 lanes
+  s0 = red[0][cl][pl];
+  s1 = red[1][cl][pl];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      s0 += red[0][i][cl];
-      s1 += red[1][i][cl];
-    }
-    store_p(dgamma, pdt, c, gamma_first ? s0 : s1);
-    store_p(dbeta, pdt, c, gamma_first ? s1 : s0);
+  for (int o = 16; o > 0; o >>= 1) {
+    s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+  }
+  const long long cc = (long long)blockIdx.x * 32 + pl;
+  if (cl == 0 && cc < ch) {
+    store_p(dgamma, pdt, cc, gamma_first ? s0 : s1);
+    store_p(dbeta, pdt, cc, gamma_first ? s1 : s0);
   }
 }
 
@@ -459,20 +504,12 @@ __global__ void __launch_bounds__(kThreads) rf_norm_apply_kernel(const __grid_co
   const int lanes = kThreads / tile, rl = threadIdx.x / tile;
   const long long c = ((long long)blockIdx.y * tile + threadIdx.x % tile) * VEC;
   if (rl >= lanes || c >= ch) return;
-  float gm[VEC], bt[VEC], mu[VEC], rs[VEC], m1[kBwd ? VEC : 1], m2[kBwd ? VEC : 1];
-#pragma unroll
-  for (int k = 0; k < VEC; ++k) {
-    const long long at = 2 * (b * (long long)a.groups + (int)(c + k) / a.width);
-    gm[k] = load_p(a.gamma, a.pdt, c + k);
-    bt[k] = load_p(a.beta, a.pdt, c + k);
-    mu[k] = a.stats[at];
-    rs[k] = a.stats[at + 1];
-    if constexpr (kBwd) {
-      const float* m = a.ws + (long long)a.batch * a.slices * 2 * ch + at;
-      m1[k] = m[0];
-      m2[k] = m[1];
-    }
-  }
+  float gm[VEC], bt[VEC], mu[VEC], rs[VEC], m1[VEC], m2[VEC];
+  load_pv<VEC>(a.gamma, a.pdt, c, gm);
+  load_pv<VEC>(a.beta, a.pdt, c, bt);
+  load_stats<VEC>(a.stats, b * (long long)a.groups, (int)c, a.width, mu, rs);
+  if constexpr (kBwd)
+    load_stats<VEC>(a.ws + (long long)a.batch * a.slices * 2 * ch, b * (long long)a.groups, (int)c, a.width, m1, m2);
   const long long xo = b * a.xs_b + chan_off(c, a.width, a.xs_g), yo = b * a.ys_b + chan_off(c, a.width, a.ys_g);
   const T* x = static_cast<const T*>(a.x) + xo;
   const T* dy = static_cast<const T*>(a.dy) + (kBwd ? yo : 0);
@@ -519,7 +556,7 @@ rf_status_t check_desc(const rf_norm_desc_t* d) {
     return rf_fail(RF_ERR_UNSUPPORTED, "more than 65535 samples");
   if (d->groups > 65535) return rf_fail(RF_ERR_UNSUPPORTED, "more than 65535 groups");
   if ((int64_t)d->groups * d->width > (1 << 30)) return rf_fail(RF_ERR_UNSUPPORTED, "too many channels");
-  if (d->rows > (1ll << 30) || d->batch * d->rows > (1ll << 40)) return rf_fail(RF_ERR_UNSUPPORTED, "too many rows");
+  if (d->rows > (1ll << 30) || d->batch > (1ll << 30) || d->batch * d->rows > (1ll << 30)) return rf_fail(RF_ERR_UNSUPPORTED, "too many rows");
   const int64_t st[] = {d->x_stride_b, d->x_stride_r, d->x_stride_g, d->y_stride_b, d->y_stride_r, d->y_stride_g};
   for (int64_t s : st)
     if (s < 0) return rf_fail(RF_ERR_INVALID_ARG, "negative stride");
@@ -545,12 +582,13 @@ bool vector_ok(const rf_norm_desc_t* d, bool rows, const void* a, const void* b,
   return true;
 }
 
-// Row slices.  Rows: four CTAs per SM over all groups (one wave), at least 32 rows each;
-// samples: two CTAs per SM, at least 32 rows each.
-int slices_of(const rf_norm_desc_t* d) {
+// Row slices: as many CTAs over all groups (channel tiles, samples) as run at
+// once, at least 32 rows each.  Rows: four per SM forward, two backward (its
+// channel sums take registers); samples: two per SM.
+int slices_of(const rf_norm_desc_t* d, bool bwd) {
   if (d->span == RF_NORM_ROW) {
     const int64_t n = d->batch * d->rows;
-    const int64_t want = std::max(1, 148 * 4 / d->groups), most = (n + 31) / 32;
+    const int64_t want = std::max(1, 148 * (bwd ? 2 : 4) / d->groups), most = (n + 31) / 32;
     return (int)std::max<int64_t>(1, std::min(want, most));
   }
   const int64_t b = std::max<int64_t>(1, d->batch);
@@ -560,13 +598,13 @@ int slices_of(const rf_norm_desc_t* d) {
 }
 
 int64_t ws_bytes_of(const rf_norm_desc_t* d) {
-  const int64_t ch = (int64_t)d->groups * d->width, sl = slices_of(d);
+  const int64_t ch = (int64_t)d->groups * d->width, sl = slices_of(d, true);
   const int64_t parts = d->span == RF_NORM_ROW ? sl : d->batch * sl;
   return (parts * 2 * ch + 2 * d->batch * d->groups) * 4 + 256;
 }
 
 NormArgs make_args(const rf_norm_desc_t* d, const void* x, const void* gamma, const void* beta, const void* dy, void* y,
-                   float* stats, void* ws) {
+                   float* stats, void* ws, bool bwd) {
   NormArgs a;
   a.x = x;
   a.gamma = gamma;
@@ -584,7 +622,7 @@ NormArgs make_args(const rf_norm_desc_t* d, const void* x, const void* gamma, co
   a.width = d->width;
   a.pdt = d->param_dtype;
   a.act = d->act;
-  a.slices = slices_of(d);
+  a.slices = slices_of(d, bwd);
   a.eps = d->eps;
   return a;
 }
@@ -629,8 +667,7 @@ rf_status_t run_samples_v(const NormArgs& a, cudaStream_t st) {
   rf_norm_partial_kernel<T, VEC, kBwd><<<dim3((unsigned)a.slices, tiles, (unsigned)a.batch), kThreads, 0, st>>>(a, tile);
   rf_status_t s = rf_check_launch("rf_norm_partial_kernel");
   if (s != RF_OK) return s;
-  if (kBwd) rf_norm_means_kernel<<<(unsigned)(a.batch * a.groups), kThreads, 0, st>>>(a);
-  else      rf_norm_stats_kernel<<<(unsigned)(a.batch * a.groups), kThreads, 0, st>>>(a);
+  rf_norm_stats_kernel<kBwd><<<(unsigned)(a.batch * a.groups), kReduceThreads, 0, st>>>(a);
   if ((s = rf_check_launch("rf_norm_stats_kernel")) != RF_OK) return s;
   const long long lanes = kThreads / tile;
   const long long most = (a.rows + lanes - 1) / lanes, want = std::max<long long>(1, 148ll * 4 / ((long long)tiles * a.batch));
@@ -689,7 +726,7 @@ rf_status_t rf_group_norm(const rf_norm_desc_t* d, const void* x, const void* ga
   if (x == y) return rf_fail(RF_ERR_INVALID_ARG, "y aliases x");
   if (sample && (st = check_norm_ws(d, ws, ws_bytes)) != RF_OK) return st;
   if ((st = rf_require_device()) != RF_OK) return st;
-  return run<false>(d, make_args(d, x, gamma, beta, nullptr, y, stats, ws), (cudaStream_t)stream);
+  return run<false>(d, make_args(d, x, gamma, beta, nullptr, y, stats, ws, false), (cudaStream_t)stream);
 }
 
 rf_status_t rf_group_norm_backward(const rf_norm_desc_t* d, const void* x, const void* gamma, const void* beta,
@@ -713,10 +750,10 @@ rf_status_t rf_group_norm_backward(const rf_norm_desc_t* d, const void* x, const
   if (dx == x || dx == dy) return rf_fail(RF_ERR_INVALID_ARG, "dx aliases an input");
   if ((st = check_norm_ws(d, ws, ws_bytes)) != RF_OK) return st;
   if ((st = rf_require_device()) != RF_OK) return st;
-  const NormArgs a = make_args(d, x, gamma, beta, dy, dx, const_cast<float*>(stats), ws);
+  const NormArgs a = make_args(d, x, gamma, beta, dy, dx, const_cast<float*>(stats), ws, true);
   if ((st = run<true>(d, a, (cudaStream_t)stream)) != RF_OK) return st;
-  rf_norm_params_kernel<<<(unsigned)((ch + 31) / 32), kThreads, 0, (cudaStream_t)stream>>>(
-      a.ws, sample ? (long long)a.batch * a.slices : (long long)a.slices, ch, sample ? 0 : 1, a.pdt, dgamma, dbeta);
+  rf_norm_params_kernel<<<(unsigned)((ch + 31) / 32), kReduceThreads, 0, (cudaStream_t)stream>>>(
+      a.ws, sample ? a.batch * a.slices : a.slices, ch, sample ? 0 : 1, a.pdt, dgamma, dbeta);
   return rf_check_launch("rf_norm_params_kernel");
 }
 
