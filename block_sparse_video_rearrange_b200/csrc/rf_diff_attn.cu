@@ -79,8 +79,9 @@ struct __align__(1024) DiffSmem {
   uint32_t tmem_base;
   int abort;
   int n_valid;
+  int first;  // this CTA's part of the list begins here
   int vexp_max;
-  float row_s[2][RF_BLOCK];  // the epilogue's factor of each map's row
+  float row_m[2][RF_BLOCK], row_l[2][RF_BLOCK];  // running maximum and sum of each map's row
   int list[RF_MAX_KV_LIST];
   int vexp[RF_MAX_KV_LIST];
 };
@@ -153,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const RfGeomDev& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int n, tb;
-  rf_cta_item(g, a.order, g.n1, blockIdx.x, n, tb);
+  const int size = (int)cluster_size(), rank = (int)cluster_rank();  // CTAs sharing this list
+  rf_cta_item(g, a.order, g.n1, blockIdx.x / size, n, tb);
   const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
   const int nblk = s.n_pb + s.nb;
   const int gk = n / (g.n1 / g.n2);
@@ -226,9 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       // A wait that already expired in this workspace stops all work.
       const bool stopped = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT) != 0;
-      sm.n_valid = stopped ? 0 : cnt;
+      sm.first = cnt * rank / size;
+      sm.n_valid = stopped ? 0 : cnt * (rank + 1) / size - sm.first;
       sm.vexp_max = vmax;
-      if (bad) atomicAdd(a.status + RF_STATUS_BAD_INDEX, (uint32_t)bad);
+      if (bad && rank == 0) atomicAdd(a.status + RF_STATUS_BAD_INDEX, (uint32_t)bad);
     }
   }
   tc_fence_before();
@@ -236,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   const int nv = sm.n_valid;
+  const int* list = sm.list + sm.first;
   const int vr_last = s.Lp - (s.n_pb - 1) * RF_BLOCK;  // valid rows of the last prefix block
   if (warp >= 8) {
     reg_dealloc<kOtherRegs>();
@@ -259,11 +263,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int c1, c2;
         if (is_k) {
           int r0, nr;
-          rf_block_span(s, sm.list[b], r0, nr);
+          rf_block_span(s, list[b], r0, nr);
           coords(g.n2, gk, r0, c1, c2);
         } else {
           c1 = 0;
-          c2 = gk * g.t_qblk + s.qblk_off + sm.list[b];
+          c2 = gk * g.t_qblk + s.qblk_off + list[b];
         }
         for (int x = 0; x < kBoxes; ++x)
           tma_load_3d(rf_smem_u32(tiles + st * kTileBytes + x * kBoxBytes),
@@ -362,16 +366,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ocol = lane_base + kOCol + (uint32_t)(w * 128);
     const float sl2 = a.sl2;
     const int vexp_max = sm.vexp_max;
+    const int* vexp = sm.vexp + sm.first;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int b = 0; b < nv; ++b) {
       if (!warp_wait(rf_smem_u32(&sm.bar_s_full[w]), b & 1, abort)) { ok = false; break; }
       tc_fence_after();
-      const int vr = (sm.list[b] == s.n_pb - 1) ? vr_last : RF_BLOCK;
+      const int vr = (list[b] == s.n_pb - 1) ? vr_last : RF_BLOCK;
       // P enters the product as P * 2^-down, the step from this V block's
       // exponent to the row's largest; it is taken inside the exponential and
       // given back to the sum.
-      const int down = min(vexp_max - sm.vexp[b], kMaxDown);
+      const int down = min(vexp_max - vexp[b], kMaxDown);
       uint32_t sr[128];
       tmem_ld32(lane_base, sr);
       tmem_ld32(lane_base + 32, sr + 32);
@@ -428,64 +433,129 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) record_timeout(abort, a.status, 3);
 
-    // Epilogue: O = 2^e_max (O_1 / l_1 - lambda O_2 / l_2); each group writes its
-    // half of the columns.
-    sm.row_s[w][r] = nv > 0 ? 1.0f / l_run : 0.f;
+    // Epilogue: O = 2^e_max (O_1 / l_1 - lambda O_2 / l_2).
+    sm.row_m[w][r] = m_run;
+    sm.row_l[w][r] = l_run;
     softmax_bar_sync();
     const bool have = nv > 0 && !*abort && warp_wait(rf_smem_u32(&sm.bar_final), 0, abort) && !*abort;
-    const float s1 = sm.row_s[0][r], s2 = sm.row_s[1][r];
     const float lam = a.lambda[n];
-    const bool live = r < q_rows;
-    const int rr = q_r0 + min(r, q_rows - 1);
-    const size_t off = rf_row_offset(g, s, g.n1, n, rr);
+    const size_t lrow = bnsd ? (size_t)s.batch_idx * s.L : (size_t)s.row_off;
+    const size_t map2 = (size_t)a.rows_total * g.n1 * D;
     if (have) tc_fence_after();
+    if (size == 1) {
+      // each group writes its half of the columns
+      const float s1 = 1.0f / sm.row_l[0][r], s2 = 1.0f / sm.row_l[1][r];
+      const bool live = r < q_rows;
+      const int rr = q_r0 + min(r, q_rows - 1);
+      const size_t off = rf_row_offset(g, s, g.n1, n, rr);
 #pragma unroll 1
-    for (int c0 = w * (D / 2); c0 < (w + 1) * (D / 2); c0 += 32) {
-      uint32_t o1[32], o2[32];
-      if (have) {
-        tmem_ld32(lane_base + kOCol + c0, o1);
-        tmem_ld32(lane_base + kOCol + 128 + c0, o2);
-        tmem_wait_ld();
+      for (int c0 = w * (D / 2); c0 < (w + 1) * (D / 2); c0 += 32) {
+        uint32_t o1[32], o2[32];
+        if (have) {
+          tmem_ld32(lane_base + kOCol + c0, o1);
+          tmem_ld32(lane_base + kOCol + 128 + c0, o2);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          o1[c] = __float_as_uint(rf_scale_pow2(s1 * __uint_as_float(o1[c]), vexp_max));
-          o2[c] = __float_as_uint(rf_scale_pow2(s2 * __uint_as_float(o2[c]), vexp_max));
+          for (int c = 0; c < 32; ++c) {
+            o1[c] = __float_as_uint(rf_scale_pow2(s1 * __uint_as_float(o1[c]), vexp_max));
+            o2[c] = __float_as_uint(rf_scale_pow2(s2 * __uint_as_float(o2[c]), vexp_max));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o1[c] = o2[c] = 0u;
         }
-      } else {
+        if (live) {
+          if constexpr (kTrain) {
+            float4* m1 = reinterpret_cast<float4*>(a.maps + off + c0);
+            float4* m2 = reinterpret_cast<float4*>(a.maps + map2 + off + c0);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) o1[c] = o2[c] = 0u;
+            for (int c = 0; c < 8; ++c) {
+              m1[c] = make_float4(__uint_as_float(o1[4 * c]), __uint_as_float(o1[4 * c + 1]),
+                                  __uint_as_float(o1[4 * c + 2]), __uint_as_float(o1[4 * c + 3]));
+              m2[c] = make_float4(__uint_as_float(o2[4 * c]), __uint_as_float(o2[4 * c + 1]),
+                                  __uint_as_float(o2[4 * c + 2]), __uint_as_float(o2[4 * c + 3]));
+            }
+          }
+          uint4* d4 = reinterpret_cast<uint4*>(a.o_r + off + c0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int e = 8 * c + 2 * i;
+              p[i] = rf_pack2<kBf16>(fmaf(-lam, __uint_as_float(o2[e]), __uint_as_float(o1[e])),
+                                     fmaf(-lam, __uint_as_float(o2[e + 1]), __uint_as_float(o1[e + 1])));
+            }
+            d4[c] = make_uint4(p[0], p[1], p[2], p[3]);
+          }
+        }
       }
-      if (live) {
+      if constexpr (kTrain) {
+        if (live)
+          a.lse[((size_t)w * g.n1 + n) * a.rows_total + lrow + rr] = have ? m_run + log2f(l_run) : INFINITY;
+      }
+    } else {
+      // group w leaves O_w where the tiles were: every product is complete, and so is
+      // every copy (that of Q is waited for where no product did)
+      if (nv == 0) {
+        volatile int no_abort = 0;
+        warp_wait(rf_smem_u32(&sm.bar_q), 0, &no_abort);
+      }
+      if (!have) sm.row_l[w][r] = 0.f;
+      const uint32_t buf = rf_smem_u32(sm.q) + (uint32_t)w * (RF_BLOCK * D * 4);
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) store_part<D, 32>(buf, ocol + c0, have, r, c0);
+    }
+    if (size > 1) {
+      cluster_sync();
+      const int rows = RF_BLOCK / size;
+      const uint32_t buf = rf_smem_u32(sm.q), am = rf_smem_u32(&sm.row_m[0][0]), al = rf_smem_u32(&sm.row_l[0][0]);
+#pragma unroll 1
+      for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+        const int row = rank * rows + i / (D / 4), c = i % (D / 4);
+        if (row >= q_rows) break;  // rows come in order
+        float o[2][4], ls[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float top = -INFINITY;
+          for (int k = 0; k < size; ++k)
+            if (cluster_ld(cluster_addr(al + 4u * (x * RF_BLOCK + row), k)) > 0.f)
+              top = fmaxf(top, cluster_ld(cluster_addr(am + 4u * (x * RF_BLOCK + row), k)));
+          float l = 0.f;
+          o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
+          for (int k = 0; k < size; ++k) {
+            const float lk = cluster_ld(cluster_addr(al + 4u * (x * RF_BLOCK + row), k));
+            if (lk == 0.f) continue;  // no entries in that part (a NaN goes on)
+            const float f = rf_ex2(cluster_ld(cluster_addr(am + 4u * (x * RF_BLOCK + row), k)) - top);
+            const float4 p = cluster_ld4(cluster_addr(buf + (uint32_t)x * (RF_BLOCK * D * 4) + part_off<D>(row, c), k));
+            l = fmaf(f, lk, l);
+            o[x][0] = fmaf(f, p.x, o[x][0]);
+            o[x][1] = fmaf(f, p.y, o[x][1]);
+            o[x][2] = fmaf(f, p.z, o[x][2]);
+            o[x][3] = fmaf(f, p.w, o[x][3]);
+          }
+          const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[x][k] = l == 0.f ? 0.f : rf_scale_pow2(inv * o[x][k], vexp_max);
+          ls[x] = l == 0.f ? INFINITY : top + log2f(l);
+        }
+        const int rr = q_r0 + row;
+        const size_t off = rf_row_offset(g, s, g.n1, n, rr) + 4 * c;
         if constexpr (kTrain) {
-          float4* m1 = reinterpret_cast<float4*>(a.maps + off + c0);
-          float4* m2 = reinterpret_cast<float4*>(a.maps + (size_t)a.rows_total * g.n1 * D + off + c0);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            m1[c] = make_float4(__uint_as_float(o1[4 * c]), __uint_as_float(o1[4 * c + 1]),
-                                __uint_as_float(o1[4 * c + 2]), __uint_as_float(o1[4 * c + 3]));
-            m2[c] = make_float4(__uint_as_float(o2[4 * c]), __uint_as_float(o2[4 * c + 1]),
-                                __uint_as_float(o2[4 * c + 2]), __uint_as_float(o2[4 * c + 3]));
-          }
+          *reinterpret_cast<float4*>(a.maps + off) = make_float4(o[0][0], o[0][1], o[0][2], o[0][3]);
+          *reinterpret_cast<float4*>(a.maps + map2 + off) = make_float4(o[1][0], o[1][1], o[1][2], o[1][3]);
+          if (c < 2) a.lse[((size_t)c * g.n1 + n) * a.rows_total + lrow + rr] = c == 0 ? ls[0] : ls[1];
         }
-        uint4* d4 = reinterpret_cast<uint4*>(a.o_r + off + c0);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t p[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = 8 * c + 2 * i;
-            p[i] = rf_pack2<kBf16>(fmaf(-lam, __uint_as_float(o2[e]), __uint_as_float(o1[e])),
-                                   fmaf(-lam, __uint_as_float(o2[e + 1]), __uint_as_float(o1[e + 1])));
-          }
-          d4[c] = make_uint4(p[0], p[1], p[2], p[3]);
-        }
+        *reinterpret_cast<uint2*>(a.o_r + off) =
+            make_uint2(rf_pack2<kBf16>(fmaf(-lam, o[1][0], o[0][0]), fmaf(-lam, o[1][1], o[0][1])),
+                       rf_pack2<kBf16>(fmaf(-lam, o[1][2], o[0][2]), fmaf(-lam, o[1][3], o[0][3])));
       }
+      cluster_sync();  // the others have read this CTA's part
     }
-    if constexpr (kTrain) {
-      if (live)
-        a.lse[((size_t)w * g.n1 + n) * a.rows_total + (bnsd ? (size_t)s.batch_idx * s.L : (size_t)s.row_off) + rr] =
-            have ? m_run + log2f(l_run) : INFINITY;
-    }
+  }
+  if (size > 1 && warp >= 8) {
+    cluster_sync();
+    cluster_sync();
   }
 
   tc_fence_before();
@@ -590,8 +660,8 @@ rf_status_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
     return rf_fail(RF_ERR_CUDA, "rf_diff_attn_kernel built with " + std::to_string(fa.numRegs) +
                                     " registers per thread; the register split needs " +
                                     std::to_string(kLaunchRegs));
-  kern<<<grid, kThreads, smem, st>>>(mq, mk, mv, args);
-  return rf_check_launch("rf_diff_attn_kernel");
+  return rf_launch_split(kern, (long long)grid, rf_split(args.g, args.g.n1, 1), kThreads, smem, st,
+                         "rf_diff_attn_kernel", mq, mk, mv, args);
 }
 
 }  // namespace

@@ -95,6 +95,7 @@ struct __align__(1024) DqSmem {
   uint32_t tmem_base;
   int abort;
   int n_valid;
+  int first;  // this CTA's part of the list begins here
   int list[RF_MAX_KV_LIST];
 };
 
@@ -173,6 +174,27 @@ __device__ __forceinline__ void store_row(uint32_t taddr, bool have, float f, bo
   }
 }
 
+// Rows [rank, rank + 1) * 128 / size of the sum over the cluster's partial
+// [128][D] buffers, times f, to 16 bits; by the 512 computing threads.
+template <int D, bool kBf16, class Row>
+__device__ __forceinline__ void merge_rows(uint32_t buf, int size, int rank, int live_rows, float f, Row row_ptr) {
+  const int rows = RF_BLOCK / size;
+  for (int i = threadIdx.x; i < rows * (D / 4); i += kCompute) {
+    const int row = rank * rows + i / (D / 4), c = i % (D / 4);
+    if (row >= live_rows) break;  // rows come in order
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < size; ++k) {
+      const float4 p = cluster_ld4(cluster_addr(buf + part_off<D>(row, c), k));
+      s.x += p.x;
+      s.y += p.y;
+      s.z += p.z;
+      s.w += p.w;
+    }
+    *reinterpret_cast<uint2*>(row_ptr(row) + 4 * c) =
+        make_uint2(rf_pack2<kBf16>(f * s.x, f * s.y), rf_pack2<kBf16>(f * s.z, f * s.w));
+  }
+}
+
 // dQ.  A step is 64 keys of a listed block.  Two sets of TMEM columns (S_1, S_2,
 // dA: 64 each at [192 p, +192)) alternate, so that a step's products run while
 // the step before is computed.  Thread = query row = TMEM lane; warpgroup e takes
@@ -201,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const RfGeomDev& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int n, tb;
-  rf_cta_item(g, a.order, g.n1, blockIdx.x, n, tb);
+  const int size = (int)cluster_size(), rank = (int)cluster_rank();  // CTAs sharing this list
+  rf_cta_item(g, a.order, g.n1, blockIdx.x / size, n, tb);
   const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
   const int nblk = s.n_pb + s.nb;
   const int gk = n / (g.n1 / g.n2);
@@ -245,7 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cnt = compact_ascending(sm.list, num, nblk, lane, &bad);
     if (lane == 0) {
       const bool stopped = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT) != 0;
-      sm.n_valid = stopped ? 0 : cnt;
+      sm.first = cnt * rank / size;
+      sm.n_valid = stopped ? 0 : cnt * (rank + 1) / size - sm.first;
     }
   }
   tc_fence_before();
@@ -253,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   const int nv = sm.n_valid;
+  const int* list = sm.list + sm.first;
   const int vr_last = s.Lp - (s.n_pb - 1) * RF_BLOCK;  // valid rows of the last prefix block
   int ea, es;
   carry_exponents<D, kBf16>(a.amax, ea, es);
@@ -277,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) record_timeout(abort, a.status, 4);
           break;
         }
-        const int blk = sm.list[t >> 1];
+        const int blk = list[t >> 1];
         // K rows past the prefix meet dS = 0 in dQ: they must be finite.
         const int left = blk == s.n_pb - 1 ? vr_last - 64 * (t & 1) : 64;
         const bool tail = left < 64;
@@ -403,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t base = lane_base + 192 * (t & 1) + 16 * e;
       // valid keys of this thread's 16 (all of them but in the partial prefix block)
-      const int vr = (sm.list[t >> 1] == s.n_pb - 1 ? vr_last : RF_BLOCK) - 64 * (t & 1) - 16 * e;
+      const int vr = (list[t >> 1] == s.n_pb - 1 ? vr_last : RF_BLOCK) - 64 * (t & 1) - 16 * e;
       uint32_t s1[16], s2[16], da[16], pk[8];
       tmem_ld16(base, s1);
       tmem_ld16(base + 64, s2);
@@ -429,8 +454,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int col = e * kN;
     const uint32_t tcol = lane_base + kDq + (D == 128 ? col : 64 * (col >> 5) + col);
     const float f = a.scale * (kBf16 ? 1.f : rf_pow2(-es));
-    store_row<kN, kBf16>(tcol, have, f, r < q_rows,
-                         a.dq + rf_row_offset(g, s, g.n1, n, q_r0 + min(r, q_rows - 1)) + col);
+    if (size == 1) {
+      store_row<kN, kBf16>(tcol, have, f, r < q_rows,
+                           a.dq + rf_row_offset(g, s, g.n1, n, q_r0 + min(r, q_rows - 1)) + col);
+    } else {
+      // the partial dQ where the tiles were (every copy and product is complete)
+      store_part<D, kN>(rf_smem_u32(sm.q), tcol, have, r, col);
+      cluster_sync();
+      merge_rows<D, kBf16>(rf_smem_u32(sm.q), size, rank, q_rows, f,
+                           [&](int row) { return a.dq + rf_row_offset(g, s, g.n1, n, q_r0 + row); });
+      cluster_sync();  // the others have read this CTA's part
+    }
+  }
+  if (size > 1 && warp >= 16) {
+    cluster_sync();
+    cluster_sync();
   }
 
   tc_fence_before();
@@ -475,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const RfGeomDev& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int gk, tb;  // tb: the key block
-  rf_cta_item(g, a.order, g.n2, blockIdx.x, gk, tb);
+  const int size = (int)cluster_size(), rank = (int)cluster_rank();  // CTAs sharing these items
+  rf_cta_item(g, a.order, g.n2, blockIdx.x / size, gk, tb);
   const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
   const int group = g.n1 / g.n2;
   int k_r0, k_rows;
@@ -522,7 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int any_stopped = __syncthreads_or(stopped ? 1 : 0);
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  const int ni = any_stopped ? 0 : sm.n_items;
+  const int i0 = sm.n_items * rank / size;  // this CTA's items: [i0, i0 + ni)
+  const int ni = any_stopped ? 0 : sm.n_items * (rank + 1) / size - i0;
   int ea, es;
   carry_exponents<D, kBf16>(a.amax, ea, es);
 
@@ -540,17 +580,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      int t = 0, tails = 0;
+      int t = 0, tails = 0, skip = i0;
       bool ok = true;
-      for (int hh = 0; ok && hh < group; ++hh) {
+      for (int hh = 0; ok && hh < group && t < 2 * ni; ++hh) {
         const int n = gk * group + hh;
         const float lam = a.lambda[n];
         const uint32_t* bw = a.bits + ((size_t)n * g.t_qblk + tb) * a.words;
-        for (int wd = 0; ok && wd < a.words; ++wd) {
+        for (int wd = 0; ok && wd < a.words && t < 2 * ni; ++wd) {
           uint32_t word = bw[wd];
-          while (ok && word) {
+          const int here = __popc(word);
+          if (skip >= here) {
+            skip -= here;
+            continue;
+          }
+          while (ok && word && t < 2 * ni) {
             const int qb = wd * 32 + __ffs(word) - 1;
             word &= word - 1;
+            if (skip > 0) {
+              --skip;
+              continue;
+            }
             int r0, nr;
             rf_block_span(s, qb, r0, nr);
             for (int h = 0; h < 2; ++h, ++t) {  // 64 rows of the query block each
@@ -797,9 +846,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int col = e * kN;
     const size_t off = rf_row_offset(g, s, g.n2, gk, k_r0 + min(r, k_rows - 1)) + col;
     const bool live = r < k_rows;
-    store_row<kN, kBf16>(lane_base + kDv + col, have, kBf16 ? 1.f : rf_pow2(-ea), live, a.dv + off);
-    store_row<kN, kBf16>(lane_base + kDk + (D == 128 ? col : 64 * (col >> 5) + col), have,
-                         a.scale * (kBf16 ? 1.f : rf_pow2(-es)), live, a.dk + off);
+    const float fv = kBf16 ? 1.f : rf_pow2(-ea), fk = a.scale * (kBf16 ? 1.f : rf_pow2(-es));
+    const uint32_t kcol = lane_base + kDk + (D == 128 ? col : 64 * (col >> 5) + col);
+    if (size == 1) {
+      store_row<kN, kBf16>(lane_base + kDv + col, have, fv, live, a.dv + off);
+      store_row<kN, kBf16>(kcol, have, fk, live, a.dk + off);
+    } else {
+      // the partial dV and dK where the tiles were (every copy and product is complete)
+      const uint32_t bv = rf_smem_u32(sm.k), bk = bv + RF_BLOCK * D * 4;
+      store_part<D, kN>(bv, lane_base + kDv + col, have, r, col);
+      store_part<D, kN>(bk, kcol, have, r, col);
+      cluster_sync();
+      merge_rows<D, kBf16>(bv, size, rank, k_rows, fv,
+                           [&](int row) { return a.dv + rf_row_offset(g, s, g.n2, gk, k_r0 + row); });
+      merge_rows<D, kBf16>(bk, size, rank, k_rows, fk,
+                           [&](int row) { return a.dk + rf_row_offset(g, s, g.n2, gk, k_r0 + row); });
+      cluster_sync();  // the others have read this CTA's part
+    }
+  }
+  if (size > 1 && warp >= 16) {
+    cluster_sync();
+    cluster_sync();
   }
 
   tc_fence_before();
@@ -971,10 +1038,11 @@ rf_status_t launch_t(const rf_plan* p, const BwdArgs& a, const void* q_r, const 
   if ((s = rf_check_launch("rf_diff_prep_bwd_kernel")) != RF_OK) return s;
   rf_diff_dlam_kernel<<<(unsigned)g.n1, 256, 0, st>>>(dlam_part, g.t_qblk, dlambda);
   if ((s = rf_check_launch("rf_diff_dlam_kernel")) != RF_OK) return s;
-  kkv<<<(unsigned)gkv, kThreads, skv, st>>>(mq[1], mk[0], mv[0], mo[1], a);
-  if ((s = rf_check_launch("rf_diff_dkv_kernel")) != RF_OK) return s;
-  kq<<<(unsigned)gq, kThreads, sq, st>>>(mq[0], mk[1], mv[1], mo[0], a);
-  return rf_check_launch("rf_diff_dq_kernel");
+  if ((s = rf_launch_split(kkv, gkv, rf_split(g, g.n2, g.n1 / g.n2), kThreads, skv, st, "rf_diff_dkv_kernel", mq[1],
+                           mk[0], mv[0], mo[1], a)) != RF_OK)
+    return s;
+  return rf_launch_split(kq, gq, rf_split(g, g.n1, 1), kThreads, sq, st, "rf_diff_dq_kernel", mq[0], mk[1], mv[1],
+                         mo[0], a);
 }
 
 }  // namespace

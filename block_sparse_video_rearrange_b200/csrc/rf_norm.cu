@@ -167,10 +167,10 @@ __device__ __forceinline__ float sub_sum(float v, int lanes) {
 // stay in registers over all rows of the CTA's slice.  kPre rows are on their
 // way from memory, unconverted, while one is computed.
 template <class T, int VEC, int NV, bool kBwd>
-__global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? (kBwd ? 2 : 4) : 1)
+__global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? (kBwd ? 3 : 4) : 1)
     rf_norm_row_kernel(const __grid_constant__ NormArgs a, int lanes) {
   constexpr int E = VEC * NV;
-  constexpr int kPre = E <= 8 ? 2 : 1;
+  constexpr int kPre = E <= 8 && !kBwd ? 2 : 1;
   using Raw = typename RawVec<T, VEC>::type;
   const int g = blockIdx.y, lane = threadIdx.x % lanes, sub = threadIdx.x / lanes, subs = kThreads / lanes;
   const T* x = static_cast<const T*>(a.x) + g * a.xs_g + lane * VEC;
@@ -583,12 +583,12 @@ bool vector_ok(const rf_norm_desc_t* d, bool rows, const void* a, const void* b,
 }
 
 // Row slices: as many CTAs over all groups (channel tiles, samples) as run at
-// once, at least 32 rows each.  Rows: four per SM forward, two backward (its
+// once, at least 32 rows each.  Rows: four per SM forward, three backward (its
 // channel sums take registers); samples: two per SM.
 int slices_of(const rf_norm_desc_t* d, bool bwd) {
   if (d->span == RF_NORM_ROW) {
     const int64_t n = d->batch * d->rows;
-    const int64_t want = std::max(1, 148 * (bwd ? 2 : 4) / d->groups), most = (n + 31) / 32;
+    const int64_t want = std::max(1, 148 * (bwd ? 3 : 4) / d->groups), most = (n + 31) / 32;
     return (int)std::max<int64_t>(1, std::min(want, most));
   }
   const int64_t b = std::max<int64_t>(1, d->batch);

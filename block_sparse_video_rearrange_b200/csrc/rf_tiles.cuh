@@ -82,6 +82,89 @@ inline RfOrder rf_order(const RfGeomDev& g) {
   return o;
 }
 
+// ---- one list over the CTAs of a cluster ---------------------------------------
+// With few (head, block) items the lists are split: the CTAs of a cluster take
+// equal consecutive parts of one list, leave their fp32 partial rows in shared
+// memory, and each merges 128 / size of the rows from all of them, in rank order.
+
+// Byte offset of 16-byte chunk c of row r in a [128][D] fp32 buffer whose chunks
+// are permuted within each row, so that neither a warp writing one chunk of 32
+// rows nor one reading a row's chunks meets bank conflicts.
+template <int D>
+__device__ __forceinline__ uint32_t part_off(int r, int c) {
+  return (uint32_t)(r * (D * 4) + ((c ^ (r & (D / 4 - 1))) << 4));
+}
+
+// N accumulator columns of this thread's row (TMEM), from column col on, into the
+// buffer at `buf`; zeros where there are none.
+template <int D, int N>
+__device__ __forceinline__ void store_part(uint32_t buf, uint32_t taddr, bool have, int r, int col) {
+  uint32_t o[N];
+  if (have) {
+    if constexpr (N == 32) tmem_ld32(taddr, o);
+    else                   tmem_ld16(taddr, o);
+    tmem_wait_ld();
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) o[c] = 0u;
+  }
+#pragma unroll
+  for (int c = 0; c < N / 4; ++c) sts128(buf + part_off<D>(r, col / 4 + c), o + 4 * c);
+}
+
+// How many CTAs share a list: the size whose estimated finish is earliest.  A CTA
+// costs about kFixed blocks' time beside its list (start, first loads, epilogue);
+// a merge two more.  The launch ends no earlier than its longest CTA and no
+// earlier than the work spread over 148 SMs.
+inline int rf_split(const RfGeomDev& g, int heads, int group) {
+  constexpr double kFixed = 4.0, kMerge = 2.0, kSms = 148.0;
+  double dense = 0, sparse = 0, dense_len = 0, sparse_len = 0, longest = 0;
+  for (int k = 0; k < g.n_seqs; ++k) {
+    const RfSeqDev& s = g.seq[k];
+    const double nkv = s.n_pb + s.nb, nd = s.dense ? nkv : s.n_pb + s.ns;
+    const double len = s.n_pb + s.ns + (s.nb ? (double)s.k * (s.nb - s.ns) / s.nb : 0.0);
+    dense += nd;
+    dense_len += nd * nkv;
+    sparse += nkv - nd;
+    sparse_len += (nkv - nd) * (len < nkv ? len : nkv);
+    if (nkv > longest) longest = nkv;
+  }
+  int best = 1;
+  double best_t = 0;
+  for (int size = 1; size <= 8; size *= 2) {
+    const double fixed = kFixed + (size > 1 ? kMerge : 0.0);
+    const double total = heads * ((dense + sparse) * size * fixed + group * (dense_len + sparse_len));
+    const double one = fixed + group * longest / size;
+    const double t = one > total / kSms ? one : total / kSms;
+    if (size == 1 || t < 0.9 * best_t) {
+      best = size;
+      best_t = t;
+    }
+  }
+  return best;
+}
+
+// Launches `kern` with `size` CTAs per cluster for each of `items`.
+template <class... Args>
+inline rf_status_t rf_launch_split(void (*kern)(Args...), long long items, int size, int threads, size_t smem,
+                                   cudaStream_t st, const char* what, Args... args) {
+  if (items * size > 0x7FFFFFFFll) return rf_fail(RF_ERR_INVALID_ARG, "grid too large");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * size));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = size > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return rf_check_launch(what);
+  return rf_check_launch(what);
+}
+
 // Compacts the `num` entries of a selectIdx row in `list` (shared memory) in
 // place, by one warp: in-range entries that are larger than every in-range
 // entry before them stay, -1 is an unused slot, and anything else (out of

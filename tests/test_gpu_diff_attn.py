@@ -24,6 +24,8 @@ CASES = {
     "tnd_gqa_empty": ("TND", "bf16", 1, [(64, 5, 16, 24), (200, 3, 10, 19), (3, 0, 0, 0)], 6, 2, 128, 0.4, 0.3, 0.1),
     "tnd_fp16_d64": ("TND", "fp16", 1, [(0, 6, 16, 16), (130, 2, 9, 8)], 3, 3, 64, 0.5, 0.1, 0.0),
     "all_empty": ("BNSD", "bf16", 1, [(10, 2, 16, 16)], 2, 1, 128, 0.0, 1.0, 0.0),
+    "many_heads": ("BNSD", "bf16", 2, [(300, 0, 0, 0)], 200, 100, 64, 0.7, 0.05, 0.0),
+    "many_heads_gqa": ("TND", "fp16", 1, [(70, 3, 16, 16), (200, 0, 0, 0)], 96, 24, 128, 0.5, 0.05, 0.0),
     "many_blocks": ("BNSD", "bf16", 1, [(5, 10, 32, 32)], 1, 1, 128, 0.3, 0.0, 0.0),
 }
 
