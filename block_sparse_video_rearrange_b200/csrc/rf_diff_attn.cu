@@ -83,7 +83,7 @@ struct __align__(1024) DiffSmem {
   int vexp_max;
   float row_m[2][RF_BLOCK], row_l[2][RF_BLOCK];  // running maximum and sum of each map's row
   int list[RF_MAX_KV_LIST];
-  int vexp[RF_MAX_KV_LIST];
+  int vexp[RF_MAX_KV_LIST];  // by block of the sequence
 };
 
 struct DiffArgs {
@@ -209,20 +209,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const size_t row_id = (size_t)tb * g.n1 + n;
   const int32_t* row = a.sel_idx + row_id * g.max_kv;
+  // The whole row, its length and every block's exponent at once: one round trip.
+  const int32_t* ve = a.v_exp + (size_t)gk * g.t_qblk + s.qblk_off;
   const int num_raw = a.sel_num[row_id];
+  const float lam = a.lambda[n];
+  for (int c = threadIdx.x; c < g.max_kv; c += kThreads) sm.list[c] = row[c];
+  for (int c = threadIdx.x; c < nblk; c += kThreads) sm.vexp[c] = ve[c];
   const int num = num_raw < 0 ? 0 : (num_raw > g.max_kv ? g.max_kv : num_raw);
-  for (int c = threadIdx.x; c < num; c += kThreads) sm.list[c] = row[c];
   __syncthreads();
   if (warp == 0) {
     int bad = (lane == 0 && num != num_raw) ? 1 : 0;
     const int cnt = compact_ascending(sm.list, num, nblk, lane, &bad);
-    const int32_t* ve = a.v_exp + (size_t)gk * g.t_qblk + s.qblk_off;
     int vmax = -1000;
-    for (int c = lane; c < cnt; c += 32) {
-      const int e = ve[sm.list[c]];
-      sm.vexp[c] = e;
-      vmax = max(vmax, e);
-    }
+    for (int c = lane; c < cnt; c += 32) vmax = max(vmax, sm.vexp[sm.list[c]]);
     vmax = __reduce_max_sync(0xffffffffu, vmax);
     bad = __reduce_add_sync(0xffffffffu, bad);
     if (lane == 0) {
@@ -366,7 +365,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ocol = lane_base + kOCol + (uint32_t)(w * 128);
     const float sl2 = a.sl2;
     const int vexp_max = sm.vexp_max;
-    const int* vexp = sm.vexp + sm.first;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int b = 0; b < nv; ++b) {
@@ -376,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P enters the product as P * 2^-down, the step from this V block's
       // exponent to the row's largest; it is taken inside the exponential and
       // given back to the sum.
-      const int down = min(vexp_max - vexp[b], kMaxDown);
+      const int down = min(vexp_max - sm.vexp[list[b]], kMaxDown);
       uint32_t sr[128];
       tmem_ld32(lane_base, sr);
       tmem_ld32(lane_base + 32, sr + 32);
@@ -438,7 +436,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.row_l[w][r] = l_run;
     softmax_bar_sync();
     const bool have = nv > 0 && !*abort && warp_wait(rf_smem_u32(&sm.bar_final), 0, abort) && !*abort;
-    const float lam = a.lambda[n];
     const size_t lrow = bnsd ? (size_t)s.batch_idx * s.L : (size_t)s.row_off;
     const size_t map2 = (size_t)a.rows_total * g.n1 * D;
     if (have) tc_fence_after();
@@ -508,43 +505,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (size > 1) {
       cluster_sync();
+      // this CTA merges rows [rank, rank + 1) * 128 / size: first each part's factor
+      // 2^(m_k - m) / l per row and map (where the V exponents were), then the parts
       const int rows = RF_BLOCK / size;
       const uint32_t buf = rf_smem_u32(sm.q), am = rf_smem_u32(&sm.row_m[0][0]), al = rf_smem_u32(&sm.row_l[0][0]);
-#pragma unroll 1
-      for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
-        const int row = rank * rows + i / (D / 4), c = i % (D / 4);
-        if (row >= q_rows) break;  // rows come in order
-        float o[2][4], ls[2];
+      float* fac = reinterpret_cast<float*>(sm.vexp);  // [size][2][rows]
+      if (threadIdx.x < 2 * rows) {
+        const int x = threadIdx.x / rows, lr = threadIdx.x - x * rows, row = rank * rows + lr;
+        float mk[8], lk[8], top = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float top = -INFINITY;
-          for (int k = 0; k < size; ++k)
-            if (cluster_ld(cluster_addr(al + 4u * (x * RF_BLOCK + row), k)) > 0.f)
-              top = fmaxf(top, cluster_ld(cluster_addr(am + 4u * (x * RF_BLOCK + row), k)));
-          float l = 0.f;
-          o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
-          for (int k = 0; k < size; ++k) {
-            const float lk = cluster_ld(cluster_addr(al + 4u * (x * RF_BLOCK + row), k));
-            if (lk == 0.f) continue;  // no entries in that part (a NaN goes on)
-            const float f = rf_ex2(cluster_ld(cluster_addr(am + 4u * (x * RF_BLOCK + row), k)) - top);
+        for (int k = 0; k < 8; ++k) {
+          mk[k] = k < size ? cluster_ld(cluster_addr(am + 4u * (x * RF_BLOCK + row), k)) : 0.f;
+          lk[k] = k < size ? cluster_ld(cluster_addr(al + 4u * (x * RF_BLOCK + row), k)) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (lk[k] != 0.f) top = fmaxf(top, mk[k]);  // 0: no entries in that part
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          mk[k] = lk[k] != 0.f ? rf_ex2(mk[k] - top) : 0.f;
+          l = fmaf(mk[k], lk[k], l);
+        }
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < size) fac[(k * 2 + x) * rows + lr] = mk[k] * inv;
+        if constexpr (kTrain) {
+          if (row < q_rows)
+            a.lse[((size_t)x * g.n1 + n) * a.rows_total + lrow + q_r0 + row] = l == 0.f ? INFINITY : top + log2f(l);
+        }
+      }
+      softmax_bar_sync();
+#pragma unroll 2
+      for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+        const int lr = i / (D / 4), row = rank * rows + lr, c = i % (D / 4);
+        if (row >= q_rows) break;  // rows come in order
+        float o[2][4] = {};
+        for (int k = 0; k < size; ++k) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float f = fac[(k * 2 + x) * rows + lr];
             const float4 p = cluster_ld4(cluster_addr(buf + (uint32_t)x * (RF_BLOCK * D * 4) + part_off<D>(row, c), k));
-            l = fmaf(f, lk, l);
             o[x][0] = fmaf(f, p.x, o[x][0]);
             o[x][1] = fmaf(f, p.y, o[x][1]);
             o[x][2] = fmaf(f, p.z, o[x][2]);
             o[x][3] = fmaf(f, p.w, o[x][3]);
           }
-          const float inv = l == 0.f ? 0.f : 1.0f / l;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[x][k] = l == 0.f ? 0.f : rf_scale_pow2(inv * o[x][k], vexp_max);
-          ls[x] = l == 0.f ? INFINITY : top + log2f(l);
         }
-        const int rr = q_r0 + row;
-        const size_t off = rf_row_offset(g, s, g.n1, n, rr) + 4 * c;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[x][k] = rf_scale_pow2(o[x][k], max(vexp_max, -200));
+        const size_t off = rf_row_offset(g, s, g.n1, n, q_r0 + row) + 4 * c;
         if constexpr (kTrain) {
           *reinterpret_cast<float4*>(a.maps + off) = make_float4(o[0][0], o[0][1], o[0][2], o[0][3]);
           *reinterpret_cast<float4*>(a.maps + map2 + off) = make_float4(o[1][0], o[1][1], o[1][2], o[1][3]);
-          if (c < 2) a.lse[((size_t)c * g.n1 + n) * a.rows_total + lrow + rr] = c == 0 ? ls[0] : ls[1];
         }
         *reinterpret_cast<uint2*>(a.o_r + off) =
             make_uint2(rf_pack2<kBf16>(fmaf(-lam, o[1][0], o[0][0]), fmaf(-lam, o[1][1], o[0][1])),
@@ -649,15 +664,13 @@ rf_status_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
                      const DiffArgs& args, unsigned grid, cudaStream_t st) {
   size_t smem = sizeof(DiffSmem<D>) + 1024;
   if (smem < 120 * 1024) smem = 120 * 1024;  // each CTA takes all 512 TMEM columns: one per SM
-  auto kern = rf_diff_attn_kernel<D, kBf16, kTrain>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return rf_check_launch("cudaFuncSetAttribute(rf_diff_attn_kernel)");
+  constexpr auto kern = rf_diff_attn_kernel<D, kBf16, kTrain>;
+  int regs = 0;
+  rf_status_t s = rf_prepare_kernel<kern>(smem, "cudaFuncSetAttribute(rf_diff_attn_kernel)", &regs);
+  if (s != RF_OK) return s;
   // The register split could never be met by a build with fewer registers.
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess)
-    return rf_check_launch("cudaFuncGetAttributes(rf_diff_attn_kernel)");
-  if (fa.numRegs != kLaunchRegs)
-    return rf_fail(RF_ERR_CUDA, "rf_diff_attn_kernel built with " + std::to_string(fa.numRegs) +
+  if (regs != kLaunchRegs)
+    return rf_fail(RF_ERR_CUDA, "rf_diff_attn_kernel built with " + std::to_string(regs) +
                                     " registers per thread; the register split needs " +
                                     std::to_string(kLaunchRegs));
   return rf_launch_split(kern, (long long)grid, rf_split(args.g, args.g.n1, 1), kThreads, smem, st,

@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t* row = a.sel_idx + row_id * g.max_kv;
   const int num_raw = a.sel_num[row_id];
   const int num = num_raw < 0 ? 0 : (num_raw > g.max_kv ? g.max_kv : num_raw);
-  for (int c = threadIdx.x; c < num; c += kThreads) sm.list[c] = row[c];
+  for (int c = threadIdx.x; c < g.max_kv; c += kThreads) sm.list[c] = row[c];
   __syncthreads();
   if (warp == 0) {
     int bad = 0;  // counted by the forward pass and the preparation
@@ -1023,11 +1023,10 @@ rf_status_t launch_t(const rf_plan* p, const BwdArgs& a, const void* q_r, const 
   size_t sq = sizeof(DqSmem<D>) + 1024, skv = sizeof(DkvSmem<D>) + 1024;
   if (sq < 120 * 1024) sq = 120 * 1024;    // each CTA takes all 512 TMEM columns: one per SM
   if (skv < 120 * 1024) skv = 120 * 1024;
-  auto kq = rf_diff_dq_kernel<D, kBf16>;
-  auto kkv = rf_diff_dkv_kernel<D, kBf16>;
-  if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sq) != cudaSuccess ||
-      cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)skv) != cudaSuccess)
-    return rf_check_launch("cudaFuncSetAttribute(rf_diff backward)");
+  constexpr auto kq = rf_diff_dq_kernel<D, kBf16>;
+  constexpr auto kkv = rf_diff_dkv_kernel<D, kBf16>;
+  if ((s = rf_prepare_kernel<kq>(sq, "cudaFuncSetAttribute(rf_diff_dq_kernel)")) != RF_OK) return s;
+  if ((s = rf_prepare_kernel<kkv>(skv, "cudaFuncSetAttribute(rf_diff_dkv_kernel)")) != RF_OK) return s;
   // one memset: the bit rows, dlambda's parts and amax lie together
   if (cudaMemsetAsync(bits, 0, (size_t)((char*)amax - (char*)bits) + 256, st) != cudaSuccess)
     return rf_check_launch("cudaMemsetAsync(rf_diff backward)");

@@ -1,6 +1,7 @@
 // librf host side: plan creation and validation (the first phase of the
 // two-phase call on the "aclnnRainFusionAttention" API page), workspace
 // layout, status reporting and the whole-path entry point.
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -86,12 +87,14 @@ rf_status_t rf_check_launch(const char* what) {
 }
 
 rf_status_t rf_require_device() {
+  static std::atomic<int> known[64];  // 1: sm_100
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return rf_fail(RF_ERR_UNSUPPORTED_DEVICE, std::string("no CUDA device: ") + cudaGetErrorString(e));
   }
+  if (dev >= 0 && dev < 64 && known[dev].load(std::memory_order_relaxed)) return RF_OK;
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
@@ -102,6 +105,7 @@ rf_status_t rf_require_device() {
     return rf_fail(RF_ERR_UNSUPPORTED_DEVICE,
                    "librf is built for sm_100a (B200); device is sm_" + std::to_string(major) +
                        std::to_string(minor));
+  if (dev >= 0 && dev < 64) known[dev].store(1, std::memory_order_relaxed);
   return RF_OK;
 }
 

@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 
+#include <atomic>
 #include <mutex>
 #include <string>
 
@@ -115,9 +116,11 @@ __device__ __forceinline__ void store_part(uint32_t buf, uint32_t taddr, bool ha
 // How many CTAs share a list: the size whose estimated finish is earliest.  A CTA
 // costs about kFixed blocks' time beside its list (start, first loads, epilogue);
 // a merge two more.  The launch ends no earlier than its longest CTA and no
-// earlier than the work spread over 148 SMs.
+// earlier than the work spread over 148 SMs.  Measured (forward, us, sizes 1 / 2 /
+// 4): 74 items of up to 37 blocks at d = 64: 67 / 41 / 45; 148 such items at
+// d = 128: 76 / 68 / 95; 656 items of up to 82 blocks: 259 / 292 / 436.
 inline int rf_split(const RfGeomDev& g, int heads, int group) {
-  constexpr double kFixed = 4.0, kMerge = 2.0, kSms = 148.0;
+  constexpr double kFixed = 7.0, kMerge = 2.0, kSms = 148.0;
   double dense = 0, sparse = 0, dense_len = 0, sparse_len = 0, longest = 0;
   for (int k = 0; k < g.n_seqs; ++k) {
     const RfSeqDev& s = g.seq[k];
@@ -142,6 +145,28 @@ inline int rf_split(const RfGeomDev& g, int heads, int group) {
     }
   }
   return best;
+}
+
+// Sets a kernel's shared-memory limit, once per device (the call takes longer than
+// a launch), and gives its registers per thread.
+template <auto kern>
+inline rf_status_t rf_prepare_kernel(size_t smem, const char* what, int* regs = nullptr) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];  // registers + 1
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return rf_check_launch(what);
+  if (dev < 0 || dev >= kDevices) return rf_fail(RF_ERR_UNSUPPORTED_DEVICE, "device ordinal beyond 64");
+  int r = known[dev].load(std::memory_order_acquire);
+  if (r == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaFuncGetAttributes(&fa, kern) != cudaSuccess)
+      return rf_check_launch(what);
+    r = fa.numRegs + 1;
+    known[dev].store(r, std::memory_order_release);
+  }
+  if (regs) *regs = r - 1;
+  return RF_OK;
 }
 
 // Launches `kern` with `size` CTAs per cluster for each of `items`.

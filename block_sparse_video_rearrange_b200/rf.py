@@ -426,7 +426,9 @@ def _call(where: str, dev: int, stream, *args) -> None:
     fn = getattr(_lib, where)
     if torch.cuda.current_device() == dev:
         st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
-        _check(fn(*args, st), where)
+        status = fn(*args, st)
+        if status != RF_OK:
+            _check(status, where)
     else:
         with torch.cuda.device(dev):
             st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
@@ -471,17 +473,38 @@ def diff_attn_workspace_bytes(plan: Plan, backward: bool = False) -> int:
     return out.value
 
 
-def _expect_attn(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, maps, lse) -> None:
-    for t, h, nm in ((q_r, plan.n1, "q_r"), (k_r, plan.n2, "k_r"), (v_r, plan.n2, "v_r")):
-        _expect(t, plan.tensor_shape(h), plan.torch_dtype, nm)
-    si, sn = plan.select_shapes()
-    _expect(select_idx, si, torch.int32, "select_idx")
-    _expect(select_num, sn, torch.int32, "select_num")
-    _expect(lam, (plan.n1,), torch.float32, "lam")
-    if maps is not None:
-        _expect(maps, (2, *plan.tensor_shape(plan.n1)), torch.float32, "maps")
-    if lse is not None:
-        _expect(lse, (2, plan.n1, int(plan.info.rows_total)), torch.float32, "lse")
+def _diff_shapes(plan: Plan):
+    """(name -> (shape, dtype)) of the tensors of differential attention on a plan, made once per plan."""
+    sh = getattr(plan, "_diff_shapes", None)
+    if sh is None:
+        q, kv, dt, f32 = plan.tensor_shape(plan.n1), plan.tensor_shape(plan.n2), plan.torch_dtype, torch.float32
+        si, sn = plan.select_shapes()
+        sh = {nm: (q, dt) for nm in ("q_r", "o_r", "do_r", "dq_r")}
+        sh.update({nm: (kv, dt) for nm in ("k_r", "v_r", "dk_r", "dv_r")})
+        sh.update(select_idx=(si, torch.int32), select_num=(sn, torch.int32), lam=((plan.n1,), f32), dlam=((plan.n1,), f32),
+                  maps=((2, *q), f32), lse=((2, plan.n1, int(plan.info.rows_total)), f32))
+        plan._diff_shapes = sh
+    return sh
+
+
+def _diff_args(plan: Plan, ws, **tensors):
+    """Check every tensor (None allowed for maps and lse) and return their device and pointers."""
+    shapes, dev, ptrs = _diff_shapes(plan), ws.get_device(), {}
+    for nm, t in tensors.items():
+        if t is None:
+            ptrs[nm] = None
+            continue
+        shape, dt = shapes[nm]
+        if t.shape != shape or t.dtype != dt:
+            raise ValueError(f"{nm}: expected {tuple(shape)} {dt}, got {tuple(t.shape)} {t.dtype}")
+        if not t.is_cuda or t.get_device() != dev:
+            raise ValueError(f"{nm} is on {t.device}, the workspace on {ws.device}")
+        if not t.is_contiguous():
+            raise ValueError("librf takes contiguous tensors")
+        ptrs[nm] = t.data_ptr()
+    if not ws.is_cuda:
+        raise ValueError("librf takes CUDA tensors")
+    return dev, ptrs
 
 
 def diff_attn(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, scale: float, o_r, ws, maps=None, lse=None,
@@ -489,24 +512,22 @@ def diff_attn(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, scale: flo
     """(softmax(scale Q_1 K_1^T) - lam softmax(scale Q_2 K_2^T)) V over the selected blocks, the maps'
     Q and K being the two halves of each head's columns (rearranged order).  maps and lse (both or
     neither) receive what diff_attn_backward needs."""
-    _expect_attn(plan, q_r, k_r, v_r, select_idx, select_num, lam, maps, lse)
-    _expect(o_r, plan.tensor_shape(plan.n1), plan.torch_dtype, "o_r")
-    dev = _device_of(q_r, k_r, v_r, select_idx, select_num, lam, o_r, ws, maps, lse)
-    _call("rf_diff_attn", dev, stream, plan.handle, _ptr(q_r), _ptr(k_r), _ptr(v_r), _ptr(select_idx), _ptr(select_num),
-          _ptr(lam), float(scale), _ptr(o_r), _ptr(maps), _ptr(lse), _ptr(ws), _bytes(ws))
+    dev, p = _diff_args(plan, ws, q_r=q_r, k_r=k_r, v_r=v_r, select_idx=select_idx, select_num=select_num, lam=lam, o_r=o_r,
+                        maps=maps, lse=lse)
+    _call("rf_diff_attn", dev, stream, plan.handle, p["q_r"], p["k_r"], p["v_r"], p["select_idx"], p["select_num"], p["lam"],
+          float(scale), p["o_r"], p["maps"], p["lse"], _ptr(ws), _bytes(ws))
 
 
 def diff_attn_backward(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, scale: float, maps, lse, do_r, dq_r, dk_r,
                        dv_r, dlam, ws, stream=None) -> None:
     """Gradients of diff_attn from do_r and what it kept (maps, lse); rearranged order."""
-    _expect_attn(plan, q_r, k_r, v_r, select_idx, select_num, lam, maps, lse)
-    for t, h, nm in ((do_r, plan.n1, "do_r"), (dq_r, plan.n1, "dq_r"), (dk_r, plan.n2, "dk_r"), (dv_r, plan.n2, "dv_r")):
-        _expect(t, plan.tensor_shape(h), plan.torch_dtype, nm)
-    _expect(dlam, (plan.n1,), torch.float32, "dlam")
-    dev = _device_of(q_r, k_r, v_r, select_idx, select_num, lam, maps, lse, do_r, dq_r, dk_r, dv_r, dlam, ws)
-    _call("rf_diff_attn_backward", dev, stream, plan.handle, _ptr(q_r), _ptr(k_r), _ptr(v_r), _ptr(select_idx),
-          _ptr(select_num), _ptr(lam), float(scale), _ptr(maps), _ptr(lse), _ptr(do_r), _ptr(dq_r), _ptr(dk_r), _ptr(dv_r),
-          _ptr(dlam), _ptr(ws), _bytes(ws))
+    if maps is None or lse is None:
+        raise ValueError("the backward pass needs the maps and lse that diff_attn kept")
+    dev, p = _diff_args(plan, ws, q_r=q_r, k_r=k_r, v_r=v_r, select_idx=select_idx, select_num=select_num, lam=lam, maps=maps,
+                        lse=lse, do_r=do_r, dq_r=dq_r, dk_r=dk_r, dv_r=dv_r, dlam=dlam)
+    _call("rf_diff_attn_backward", dev, stream, plan.handle, p["q_r"], p["k_r"], p["v_r"], p["select_idx"], p["select_num"],
+          p["lam"], float(scale), p["maps"], p["lse"], p["do_r"], p["dq_r"], p["dk_r"], p["dv_r"], p["dlam"], _ptr(ws),
+          _bytes(ws))
 
 
 def rearrange_rows(plan: Plan, x, y, inverse: bool = False, stream=None) -> None:
