@@ -4,12 +4,13 @@ The compute path lives in the CUDA library `librf.so` (built from `csrc/`),
 reached through `block_sparse_video_rearrange_b200.rf` (ctypes binding).
 `ulysses` shards one layer over a process group by heads (sequence <-> head
 all-to-all around the path); `pipeline` runs host tensors in head chunks
-whose copies overlap the compute.  `synth` holds the seeded synthetic input
+whose copies overlap the compute.  `diff` is differential attention on the
+same path, and the group norm that follows it.  `synth` holds the seeded synthetic input
 generator.
 """
 import importlib
 
-__all__ = ["rf", "synth", "ulysses", "pipeline"]
+__all__ = ["rf", "synth", "ulysses", "pipeline", "diff"]
 
 
 def __getattr__(name):

@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <string>
+#include <utility>
 
 #include "rf_device.cuh"
 
@@ -563,6 +564,21 @@ rf_status_t check_desc(const rf_norm_desc_t* d) {
   return RF_OK;
 }
 
+// Whether no two elements of an output with these strides share a place: taken
+// from the smallest stride up, each axis steps over all that the smaller ones
+// reach (true for every permuted, padded or sliced dense tensor).
+bool disjoint(const rf_norm_desc_t* d, int64_t sb, int64_t sr, int64_t sg) {
+  std::pair<int64_t, int64_t> ax[3] = {{sb, d->batch}, {sr, d->rows}, {sg, d->groups}};
+  std::sort(ax, ax + 3);
+  int64_t reach = d->width;
+  for (const auto& a : ax) {
+    if (a.second <= 1) continue;
+    if (a.first < reach) return false;
+    reach += (a.second - 1) * a.first;
+  }
+  return true;
+}
+
 int vec_of(const rf_norm_desc_t* d) { return d->dtype == RF_FP32 ? 4 : 8; }
 
 // Channels per thread: 16-byte vectors where every row and group begins on one.
@@ -724,6 +740,8 @@ rf_status_t rf_group_norm(const rf_norm_desc_t* d, const void* x, const void* ga
   if (d->batch == 0 || d->rows == 0) return RF_OK;
   if (!x || !y || (sample && !stats)) return rf_fail(RF_ERR_INVALID_ARG, "null tensor");
   if (x == y) return rf_fail(RF_ERR_INVALID_ARG, "y aliases x");
+  if (!disjoint(d, d->y_stride_b, d->y_stride_r, d->y_stride_g))
+    return rf_fail(RF_ERR_INVALID_ARG, "elements of y overlap (a broadcast output)");
   if (sample && (st = check_norm_ws(d, ws, ws_bytes)) != RF_OK) return st;
   if ((st = rf_require_device()) != RF_OK) return st;
   return run<false>(d, make_args(d, x, gamma, beta, nullptr, y, stats, ws, false), (cudaStream_t)stream);
@@ -748,6 +766,8 @@ rf_status_t rf_group_norm_backward(const rf_norm_desc_t* d, const void* x, const
   }
   if (!x || !dy || !dx || (sample && !stats)) return rf_fail(RF_ERR_INVALID_ARG, "null tensor");
   if (dx == x || dx == dy) return rf_fail(RF_ERR_INVALID_ARG, "dx aliases an input");
+  if (!disjoint(d, d->x_stride_b, d->x_stride_r, d->x_stride_g))
+    return rf_fail(RF_ERR_INVALID_ARG, "elements of dx overlap (x is broadcast)");
   if ((st = check_norm_ws(d, ws, ws_bytes)) != RF_OK) return st;
   if ((st = rf_require_device()) != RF_OK) return st;
   const NormArgs a = make_args(d, x, gamma, beta, dy, dx, const_cast<float*>(stats), ws, true);

@@ -512,7 +512,7 @@ typedef struct {
 RF_API rf_status_t rf_group_norm_workspace_bytes(const rf_norm_desc_t* desc, int64_t* out);
 /* stats: RF_NORM_SAMPLE: fp32 [batch, groups, 2], receives {mu, 1 / sqrt(var +
  * eps)}, which the backward pass reads; RF_NORM_ROW: may be NULL (and so may ws).
- * Outputs must not overlap inputs. */
+ * Outputs must not overlap inputs, nor (by zero or small strides) themselves. */
 RF_API rf_status_t rf_group_norm(const rf_norm_desc_t* desc, const void* x, const void* gamma,
                                  const void* beta, void* y, float* stats, void* ws,
                                  size_t ws_bytes, rf_stream_t stream);

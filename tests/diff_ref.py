@@ -2,8 +2,12 @@
 
 Rounding steps (relative, at most): the output's or gradient's own rounding u = eps / 2 of its type; P to f16 in the
 forward product, 2^-11; A and dS to the tensors' type in the backward products, u.  FP32 covers the rest: scores of at
-most 64 in log2 units carry an absolute error under 64 * 2^-22 there, so the exponentials are off by less than 2^-15,
-and with their sums, the products' accumulation and ex2's own 2^-22 by less than FP32 = 2^-13.
+most 400 in log2 units carry an absolute error under 400 * 2^-22 there, so the exponentials are off by less than
+2^-13.8, and with their sums, the products' accumulation and ex2's own 2^-22 by less than FP32 = 2^-13.
+
+fp16 has a smallest step too: 2^-24, so a rounding there is off by 2^-25 at most whatever the value.  For the results
+that is the floor itself; A carries at least 2^12 through its rounding, and dS the power of two that takes its bound
+B = 2 d max|dO| max|V| max(1, |lambda|) to at most 2^15, i.e. at least 2^14 / B: their floors are smaller by that.
 """
 import torch
 
@@ -64,7 +68,14 @@ def selection(plan, gen, keep=0.5, empty=0.0, unused=0.0):
 def reference(plan, q, k, v, idx, num, lam, scale, do=None):
     """{"o", "maps", "lse"} and, with do, {"dq", "dk", "dv", "dlam"}, each with a bound "<name>_tol" per element."""
     dt = q.dtype
+    # an fp16 result below 2^-14 is rounded to a multiple of 2^-24 (fp16's subnormal numbers): by at most 2^-25,
+    # whatever its size (bf16 has fp32's exponents and no such floor here)
+    floor = 2.0 ** -25 if dt == torch.float16 else 0.0
     u, h, rep = half_step(dt), plan.d // 2, plan.n1 // plan.n2
+    ds_floor = 0.0
+    if do is not None and floor:
+        bound = 2 * plan.d * float(do.double().abs().max()) * float(v.double().abs().max()) * max(1.0, float(lam.abs().max()))
+        ds_floor = floor * bound * 2.0 ** -14
     q, k, v = (flat(plan, x) for x in (q, k, v))
     dev = q.device
     o, o_tol = torch.zeros_like(q), torch.zeros_like(q)
@@ -93,7 +104,7 @@ def reference(plan, q, k, v, idx, num, lam, scale, do=None):
                 e = [(P_STEP + FP32) * (x @ vv.abs()) + P_TINY * t * vv.abs().sum(0) for x, t in zip(p, tops)]
                 o[hd, sl] = ow[0] - la * ow[1]
                 e_o = e[0] + abs(la) * e[1]
-                o_tol[hd, sl] = u * (o[hd, sl].abs() + e_o) + e_o
+                o_tol[hd, sl] = u * (o[hd, sl].abs() + e_o) + e_o + floor
                 for w in (0, 1):
                     maps[w, hd, sl], maps_tol[w, hd, sl] = ow[w], e[w]
                     lse[w, hd, sl] = torch.logsumexp(s[w], 1) / torch.log(torch.tensor(2.0, dtype=torch.float64))
@@ -111,7 +122,7 @@ def reference(plan, q, k, v, idx, num, lam, scale, do=None):
                     delta = (p[w] * da).sum(1, keepdim=True)
                     ds = c * p[w] * (da - delta)
                     d_err = (up.abs() * e[w]).sum(1, keepdim=True) + FP32 * (p[w] * da_abs).sum(1, keepdim=True)
-                    err = u * ds.abs() + (1 + u) * abs(c) * p[w] * (d_err + FP32 * (da_abs + delta.abs()))
+                    err = u * ds.abs() + (1 + u) * abs(c) * p[w] * (d_err + FP32 * (da_abs + delta.abs())) + ds_floor
                     cols = slice(w * h, w * h + h)
                     dq[hd, sl, cols] = scale * (ds @ kk[:, cols])
                     dq_tol[hd, sl, cols] = scale * (err @ kk[:, cols].abs())
@@ -123,6 +134,6 @@ def reference(plan, q, k, v, idx, num, lam, scale, do=None):
     out = dict(o=back(plan, o), o_tol=back(plan, o_tol), maps=maps, maps_tol=maps_tol, lse=lse)
     if do is not None:
         for nm, x, t in (("dq", dq, dq_tol), ("dk", dk, dk_tol), ("dv", dv, dv_tol)):
-            out[nm], out[nm + "_tol"] = back(plan, x), back(plan, t + u * (x.abs() + t))
+            out[nm], out[nm + "_tol"] = back(plan, x), back(plan, t + u * (x.abs() + t) + floor)
         out["dlam"], out["dlam_tol"] = dlam, dlam_tol
     return out
