@@ -10,7 +10,7 @@
 // left.  For the same reason P enters the product as f16 (11 significant bits)
 // whatever the input type: with bf16 inputs and near-uniform maps a bf16 P
 // gives a relative error of 6e-3, an f16 P under 2e-3, of which 1.65e-3 is the
-// output's own rounding.  tcgen05.mma takes A and B of one type, so V is read
+// output's own rounding (short fp16 lists: see kFineBlocks).  tcgen05.mma takes A and B of one type, so V is read
 // from f16 copies by block (rf_diff_prep_v_kernel): v * 2^-e, exact for every
 // value down to 2^-29 of the block's largest, with the rows past a block's end
 // zero (an unselected row's NaN must not meet P = 0).
@@ -60,6 +60,12 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays at or below 2^
 // to zero in f16 (P <= 2^8, f16's last bit 2^-24).
 constexpr int kMaxDown = 40;
 constexpr uint32_t kBoxBytes = RF_BLOCK * 128;
+// fp16 lists of up to this many blocks take P in two f16 parts, twice the P V
+// products: there a CTA's fixed cost hides them (77 and 300 keys: 14.3 and 21.1 us
+// either way), while on a long list they set the time (2.48 against 4.15 ms, 5
+// heads of the Wan-shaped grid), for fp16 results at their own rounding, 2e-4,
+// instead of 7e-4 where the maps are near-uniform.
+constexpr int kFineBlocks = 8;
 
 template <int D>
 struct __align__(1024) DiffSmem {
@@ -73,6 +79,7 @@ struct __align__(1024) DiffSmem {
   uint64_t bar_s_full[2];                 // S of (b, w) computed, one barrier per map
   uint64_t bar_s_free;                    // S read into registers
   uint64_t bar_p_half[2], bar_p_full[2];  // P of map w stored, first half / all
+  uint64_t bar_ph_done[2];                // two parts: the first half's products complete, its P columns free
   uint64_t bar_pv_done[2];                // O_w += P_w V_b complete
   uint64_t bar_final;
   uint64_t bar_drain;
@@ -81,6 +88,7 @@ struct __align__(1024) DiffSmem {
   int n_valid;
   int first;  // this CTA's part of the list begins here
   int vexp_max;
+  int fine;   // P in two f16 parts
   float row_m[2][RF_BLOCK], row_l[2][RF_BLOCK];  // running maximum and sum of each map's row
   int list[RF_MAX_KV_LIST];
   int vexp[RF_MAX_KV_LIST];  // by block of the sequence
@@ -127,6 +135,29 @@ __device__ __forceinline__ void quarter_exp(const uint32_t* sr, int c0, int vr, 
     pk[c >> 1] = rf_pack2<false>(p0, p1);
   }
   tmem_st16(p_addr, pk);
+}
+
+// The same for an fp16 list in two parts: the f16 values at p_addr, what their
+// rounding left, as f16 too, 32 columns on.
+__device__ __forceinline__ void quarter_exp_fine(const uint32_t* sr, int c0, int vr, float sl2, float neg_m,
+                                                 uint32_t p_addr, uint64_t* acc) {
+  const uint64_t sl2x2 = rf_f2(__float_as_uint(sl2), __float_as_uint(sl2));
+  const uint64_t negm2 = rf_f2(__float_as_uint(neg_m), __float_as_uint(neg_m));
+  uint32_t pk[16], lo[16];
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    float x0, x1;
+    rf_f2_split(rf_fma2(rf_f2(sr[c0 + c], sr[c0 + c + 1]), sl2x2, negm2), x0, x1);
+    float p0 = rf_ex2(x0), p1 = rf_ex2(x1);
+    p0 = c0 + c < vr ? p0 : 0.f;
+    p1 = c0 + c + 1 < vr ? p1 : 0.f;
+    acc[(c >> 1) & 3] = rf_add2(acc[(c >> 1) & 3], rf_f2(__float_as_uint(p0), __float_as_uint(p1)));
+    pk[c >> 1] = rf_pack2<false>(p0, p1);
+    const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pk[c >> 1]));
+    lo[c >> 1] = rf_pack2<false>(p0 - r.x, p1 - r.y);
+  }
+  tmem_st16(p_addr, pk);
+  tmem_st16(p_addr + 32, lo);
 }
 
 __device__ __forceinline__ float acc_sum(const uint64_t* acc) {
@@ -176,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(rf_smem_u32(&sm.bar_s_full[i]), 1);
       mbar_init(rf_smem_u32(&sm.bar_p_half[i]), 128);
       mbar_init(rf_smem_u32(&sm.bar_p_full[i]), 128);
+      mbar_init(rf_smem_u32(&sm.bar_ph_done[i]), 1);
       mbar_init(rf_smem_u32(&sm.bar_pv_done[i]), 1);
     }
     mbar_init(rf_smem_u32(&sm.bar_s_free), 128);
@@ -230,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm.first = cnt * rank / size;
       sm.n_valid = stopped ? 0 : cnt * (rank + 1) / size - sm.first;
       sm.vexp_max = vmax;
+      sm.fine = !kBf16 && cnt <= kFineBlocks;
       if (bad && rank == 0) atomicAdd(a.status + RF_STATUS_BAD_INDEX, (uint32_t)bad);
     }
   }
@@ -239,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   const int nv = sm.n_valid;
   const int* list = sm.list + sm.first;
+  const bool fine = !kBf16 && sm.fine;
   const int vr_last = s.Lp - (s.n_pb - 1) * RF_BLOCK;  // valid rows of the last prefix block
   if (warp >= 8) {
     reg_dealloc<kOtherRegs>();
@@ -325,16 +359,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < RF_BLOCK / 32; ++kk)
+            for (int kk = 0; kk < 4; ++kk)
               mma_ts(d_o, a_p + kk * 8, dv + (uint32_t)(kk * (2048 >> 4)), idesc, (b > 0 || kk > 0) ? 1u : 0u);
+            if (fine) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) mma_ts(d_o, a_p + 32 + kk * 8, dv + (uint32_t)(kk * (2048 >> 4)), idesc, 1u);
+              tc_commit(rf_smem_u32(&sm.bar_ph_done[w]));
+            }
           }
           __syncwarp();
           if (!warp_wait<true>(rf_smem_u32(&sm.bar_p_full[w]), b & 1, abort)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
+            const uint32_t a_p2 = fine ? a_p : a_p + 32;
 #pragma unroll
-            for (int kk = RF_BLOCK / 32; kk < RF_BLOCK / 16; ++kk)
-              mma_ts(d_o, a_p + kk * 8, dv + (uint32_t)(kk * (2048 >> 4)), idesc, 1u);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(d_o, a_p2 + kk * 8, dv + (uint32_t)((kk + 4) * (2048 >> 4)), idesc, 1u);
+            if (fine) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(d_o, a_p + 32 + kk * 8, dv + (uint32_t)((kk + 4) * (2048 >> 4)), idesc, 1u);
+            }
             if (w == 1) tc_commit(rf_smem_u32(&sm.bar_v_empty[st]));
             tc_commit(rf_smem_u32(&sm.bar_pv_done[w]));
           }
@@ -407,22 +452,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
       const float neg_m = -m_run - (float)down;
-      if (vr == RF_BLOCK) {
-        quarter_exp<true>(sr, 0, vr, sl2, neg_m, pcol, acc);
-        quarter_exp<true>(sr, 32, vr, sl2, neg_m, pcol + 16, acc);
+      if (fine) {
+        // a half's two parts fill the map's P columns: the second half's go there
+        // when the first half's products are complete
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(rf_smem_u32(&sm.bar_p_half[w]));
+            if (!warp_wait(rf_smem_u32(&sm.bar_ph_done[w]), b & 1, abort)) { ok = false; break; }
+            tc_fence_after();
+          }
+          quarter_exp_fine(sr, 64 * h, vr, sl2, neg_m, pcol, acc);
+          quarter_exp_fine(sr, 64 * h + 32, vr, sl2, neg_m, pcol + 16, acc);
+        }
+        if (!ok) break;
       } else {
-        quarter_exp<false>(sr, 0, vr, sl2, neg_m, pcol, acc);
-        quarter_exp<false>(sr, 32, vr, sl2, neg_m, pcol + 16, acc);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(rf_smem_u32(&sm.bar_p_half[w]));
-      if (vr == RF_BLOCK) {
-        quarter_exp<true>(sr, 64, vr, sl2, neg_m, pcol + 32, acc);
-        quarter_exp<true>(sr, 96, vr, sl2, neg_m, pcol + 48, acc);
-      } else {
-        quarter_exp<false>(sr, 64, vr, sl2, neg_m, pcol + 32, acc);
-        quarter_exp<false>(sr, 96, vr, sl2, neg_m, pcol + 48, acc);
+        if (vr == RF_BLOCK) {
+          quarter_exp<true>(sr, 0, vr, sl2, neg_m, pcol, acc);
+          quarter_exp<true>(sr, 32, vr, sl2, neg_m, pcol + 16, acc);
+        } else {
+          quarter_exp<false>(sr, 0, vr, sl2, neg_m, pcol, acc);
+          quarter_exp<false>(sr, 32, vr, sl2, neg_m, pcol + 16, acc);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(rf_smem_u32(&sm.bar_p_half[w]));
+        if (vr == RF_BLOCK) {
+          quarter_exp<true>(sr, 64, vr, sl2, neg_m, pcol + 32, acc);
+          quarter_exp<true>(sr, 96, vr, sl2, neg_m, pcol + 48, acc);
+        } else {
+          quarter_exp<false>(sr, 64, vr, sl2, neg_m, pcol + 32, acc);
+          quarter_exp<false>(sr, 96, vr, sl2, neg_m, pcol + 48, acc);
+        }
       }
       l_run += acc_sum(acc) * rf_pow2(down);
       tmem_wait_st();
