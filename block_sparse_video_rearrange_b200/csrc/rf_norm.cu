@@ -146,13 +146,24 @@ __device__ __forceinline__ void load_stats(const float* st, long long first_grou
   }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// 1 / (1 + e^-z) from the ex2 and reciprocal units (2^-21 relative together).
+__device__ __forceinline__ float sigmoid(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + rf_ex2(-1.4426950408889634f * z)));
+  return r;
+}
 __device__ __forceinline__ float act_f(float z, int act) { return act == RF_ACT_SILU ? z * sigmoid(z) : z; }
 // derivative of the activation at z
 __device__ __forceinline__ float act_d(float z, int act) {
   if (act != RF_ACT_SILU) return 1.f;
   const float s = sigmoid(z);
   return s * fmaf(z, 1.f - s, 1.f);
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) { return rf_f2(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float pair_sum(uint64_t p) {
+  float a, b;
+  rf_f2_split(p, a, b);
+  return a + b;
 }
 
 // Sum over the `lanes` (a power of two) neighbouring lanes of a sub-warp.
@@ -177,16 +188,23 @@ __global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? (kBwd ? 3 : 4) : 1)
   const T* x = static_cast<const T*>(a.x) + g * a.xs_g + lane * VEC;
   const T* dy = static_cast<const T*>(a.dy) + g * a.ys_g + lane * VEC;
   T* out = static_cast<T*>(a.y) + (kBwd ? g * a.xs_g : g * a.ys_g) + lane * VEC;
-  float gm[E], bt[E], sg[kBwd ? E : 1], sb[kBwd ? E : 1];
+  // channels in pairs for the paired fp32 instructions (a lone channel beside a zero)
+  constexpr int P = (E + 1) / 2;
+  uint64_t gm[P], bt[P], sg[kBwd ? P : 1], sb[kBwd ? P : 1];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * lanes + lane) * VEC;
+  for (int p = 0; p < P; ++p) {
+    float g2[2] = {0.f, 0.f}, b2[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      gm[v * VEC + i] = c < a.width ? load_p(a.gamma, a.pdt, (long long)g * a.width + c + i) : 0.f;
-      bt[v * VEC + i] = c < a.width ? load_p(a.beta, a.pdt, (long long)g * a.width + c + i) : 0.f;
-      if constexpr (kBwd) sg[v * VEC + i] = sb[v * VEC + i] = 0.f;
+    for (int i = 0; i < 2; ++i) {
+      const int k = 2 * p + i, c = (k / VEC * lanes + lane) * VEC + k % VEC;
+      if (k < E && c < a.width) {
+        g2[i] = load_p(a.gamma, a.pdt, (long long)g * a.width + c);
+        b2[i] = load_p(a.beta, a.pdt, (long long)g * a.width + c);
+      }
     }
+    gm[p] = pair(g2[0], g2[1]);
+    bt[p] = pair(b2[0], b2[1]);
+    if constexpr (kBwd) sg[p] = sb[p] = 0ull;
   }
   const int mine = (a.width / VEC - lane + lanes - 1) / lanes;  // vectors of this lane (v < mine)
   const float inv = 1.0f / (float)a.width;
@@ -225,50 +243,89 @@ __global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? (kBwd ? 3 : 4) : 1)
     for (int w = 0; w < kPre; ++w) {
       const int i = i0 + w;
       const bool live = sub + i * subs < n_mine;
-      float xv[E], dv[kBwd ? E : 1];
+      uint64_t xp[P], dp[kBwd ? P : 1];
+      {
+        float f[2 * P];
+        f[2 * P - 1] = 0.f;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        unpack_v<T, VEC>(xr[w][v], xv + v * VEC);
-        if constexpr (kBwd) unpack_v<T, VEC>(dr[w][v], dv + v * VEC);
+        for (int v = 0; v < NV; ++v) unpack_v<T, VEC>(xr[w][v], f + v * VEC);
+#pragma unroll
+        for (int p = 0; p < P; ++p) xp[p] = pair(f[2 * p], f[2 * p + 1]);
+        if constexpr (kBwd) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v) unpack_v<T, VEC>(dr[w][v], f + v * VEC);
+#pragma unroll
+          for (int p = 0; p < P; ++p) dp[p] = pair(f[2 * p], f[2 * p + 1]);
+        }
       }
       load(i + kPre, w);
-      float s = 0.f;
+      uint64_t s2 = xp[0];
 #pragma unroll
-      for (int k = 0; k < E; ++k) s += xv[k];
-      const float mu = sub_sum(s, lanes) * inv;
-      s = 0.f;
+      for (int p = 1; p < P; ++p) s2 = rf_add2(s2, xp[p]);
+      const float mu = sub_sum(pair_sum(s2), lanes) * inv;
+      s2 = 0ull;
 #pragma unroll
-      for (int k = 0; k < E; ++k) {
-        xv[k] = k / VEC < mine ? xv[k] - mu : 0.f;
-        s = fmaf(xv[k], xv[k], s);
+      for (int p = 0; p < P; ++p) {
+        // vectors that this lane does not have stay zero
+        const float m0 = 2 * p / VEC < mine ? -mu : 0.f;
+        const float m1 = 2 * p + 1 < E && (2 * p + 1) / VEC < mine ? -mu : 0.f;
+        xp[p] = rf_add2(xp[p], pair(m0, m1));
+        s2 = rf_fma2(xp[p], xp[p], s2);
       }
-      const float rstd = rsqrtf(sub_sum(s, lanes) * inv + a.eps);
+      float rstd = rsqrtf(sub_sum(pair_sum(s2), lanes) * inv + a.eps);
+      if (!live) rstd = 0.f;  // a row past the end counts for nothing, even with eps = 0
+      const uint64_t rs2 = pair(rstd, rstd);
       if constexpr (!kBwd) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) xv[k] = act_f(fmaf(xv[k] * rstd, gm[k], bt[k]), a.act);
-      } else {
-        float m1 = 0.f, m2 = 0.f;
+        for (int p = 0; p < P; ++p) xp[p] = rf_fma2(rf_mul2(xp[p], rs2), gm[p], bt[p]);
+        if (a.act == RF_ACT_SILU) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          xv[k] *= rstd;
-          // a row past the end has dy = 0, and so g = 0, unless eps = 0 makes its xh NaN
-          const float gz = live ? dv[k] * act_d(fmaf(xv[k], gm[k], bt[k]), a.act) : 0.f;
-          sg[k] = live ? fmaf(gz, xv[k], sg[k]) : sg[k];
-          sb[k] += gz;
-          dv[k] = gz * gm[k];
-          m1 += dv[k];
-          m2 = fmaf(dv[k], xv[k], m2);
+          for (int p = 0; p < P; ++p) {
+            float z0, z1;
+            rf_f2_split(xp[p], z0, z1);
+            xp[p] = pair(z0 * sigmoid(z0), z1 * sigmoid(z1));
+          }
         }
-        m1 = sub_sum(m1, lanes) * inv;
-        m2 = sub_sum(m2, lanes) * inv;
+      } else {
+        uint64_t m1 = 0ull, m2 = 0ull;
+        if (a.act == RF_ACT_SILU) {
+          const uint64_t one = pair(1.f, 1.f), neg = pair(-1.f, -1.f);
 #pragma unroll
-        for (int k = 0; k < E; ++k) xv[k] = rstd * (dv[k] - m1 - xv[k] * m2);
+          for (int p = 0; p < P; ++p) {
+            const uint64_t z = rf_fma2(rf_mul2(xp[p], rs2), gm[p], bt[p]);
+            float z0, z1;
+            rf_f2_split(z, z0, z1);
+            const uint64_t s = pair(sigmoid(z0), sigmoid(z1));
+            // act'(z) = s (1 + z (1 - s))
+            dp[p] = rf_mul2(dp[p], rf_mul2(s, rf_fma2(z, rf_fma2(s, neg, one), one)));
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          xp[p] = rf_mul2(xp[p], rs2);
+          sg[p] = rf_fma2(dp[p], xp[p], sg[p]);
+          sb[p] = rf_add2(sb[p], dp[p]);
+          dp[p] = rf_mul2(dp[p], gm[p]);
+          m1 = rf_add2(m1, dp[p]);
+          m2 = rf_fma2(dp[p], xp[p], m2);
+        }
+        const float u1 = -sub_sum(pair_sum(m1), lanes) * inv * rstd, u2 = -sub_sum(pair_sum(m2), lanes) * inv * rstd;
+        const uint64_t v1 = pair(u1, u1), v2 = pair(u2, u2);
+        // dx = rstd g - rstd mean(g) - xh rstd mean(g xh)
+#pragma unroll
+        for (int p = 0; p < P; ++p) xp[p] = rf_fma2(xp[p], v2, rf_fma2(dp[p], rs2, v1));
       }
       if (live) {
         T* po = out + (kBwd ? sb_ * a.xs_b + sr * a.xs_r : sb_ * a.ys_b + sr * a.ys_r);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-          if (v < mine) store_v<T, VEC>(po + v * lanes * VEC, xv + v * VEC);
+          if (v < mine) {
+            float f[VEC + 1];
+#pragma unroll
+            for (int k = 0; k < VEC; k += 2) rf_f2_split(xp[(v * VEC + k) / 2], f[k], f[k + 1]);
+            if (VEC == 1 && v % 2) f[0] = f[1];
+            store_v<T, VEC>(po + v * lanes * VEC, f);
+          }
       }
       sr += subs;
       while (sr >= n_r) {
@@ -288,8 +345,11 @@ __global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? (kBwd ? 3 : 4) : 1)
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
               const int c = (v * lanes + lane) * VEC + k;
-              red[0][c] = (turn ? red[0][c] : 0.f) + sg[v * VEC + k];
-              red[1][c] = (turn ? red[1][c] : 0.f) + sb[v * VEC + k];
+              float g2[2], b2[2];
+              rf_f2_split(sg[(v * VEC + k) / 2], g2[0], g2[1]);
+              rf_f2_split(sb[(v * VEC + k) / 2], b2[0], b2[1]);
+              red[0][c] = (turn ? red[0][c] : 0.f) + g2[(v * VEC + k) % 2];
+              red[1][c] = (turn ? red[1][c] : 0.f) + b2[(v * VEC + k) % 2];
             }
       }
       __syncthreads();
