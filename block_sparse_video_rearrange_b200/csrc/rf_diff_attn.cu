@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t* ve = a.v_exp + (size_t)gk * g.t_qblk + s.qblk_off;
   const int num_raw = a.sel_num[row_id];
   const float lam = a.lambda[n];
+  const uint32_t expired = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT);
   for (int c = threadIdx.x; c < g.max_kv; c += kThreads) sm.list[c] = row[c];
   for (int c = threadIdx.x; c < nblk; c += kThreads) sm.vexp[c] = ve[c];
   const int num = num_raw < 0 ? 0 : (num_raw > g.max_kv ? g.max_kv : num_raw);
@@ -257,8 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     vmax = __reduce_max_sync(0xffffffffu, vmax);
     bad = __reduce_add_sync(0xffffffffu, bad);
     if (lane == 0) {
-      // A wait that already expired in this workspace stops all work.
-      const bool stopped = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT) != 0;
+      const bool stopped = expired != 0;  // a wait that already expired in this workspace stops all work
       sm.first = cnt * rank / size;
       sm.n_valid = stopped ? 0 : cnt * (rank + 1) / size - sm.first;
       sm.vexp_max = vmax;
@@ -502,67 +502,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     const size_t lrow = bnsd ? (size_t)s.batch_idx * s.L : (size_t)s.row_off;
     const size_t map2 = (size_t)a.rows_total * g.n1 * D;
     if (have) tc_fence_after();
+    const uint32_t parts = rf_smem_u32(sm.q);  // [2][128][D] fp32 where the tiles were
+    if (nv == 0) {  // every product is complete, and so is every copy but that of Q where no product waited for it
+      volatile int no_abort = 0;
+      warp_wait(rf_smem_u32(&sm.bar_q), 0, &no_abort);
+    }
     if (size == 1) {
-      // each group writes its half of the columns
-      const float s1 = 1.0f / sm.row_l[0][r], s2 = 1.0f / sm.row_l[1][r];
-      const bool live = r < q_rows;
-      const int rr = q_r0 + min(r, q_rows - 1);
-      const size_t off = rf_row_offset(g, s, g.n1, n, rr);
+      // Through shared memory, so that whole rows leave in one piece: written by the
+      // row's own thread, 16 bytes here and there, the two fp32 maps took 11,000
+      // cycles a CTA (now 2,000).
+      const float f = have ? 1.0f / l_run : 0.f;
 #pragma unroll 1
-      for (int c0 = w * (D / 2); c0 < (w + 1) * (D / 2); c0 += 32) {
-        uint32_t o1[32], o2[32];
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t o[32];
         if (have) {
-          tmem_ld32(lane_base + kOCol + c0, o1);
-          tmem_ld32(lane_base + kOCol + 128 + c0, o2);
+          tmem_ld32(ocol + c0, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            o1[c] = __float_as_uint(rf_scale_pow2(s1 * __uint_as_float(o1[c]), vexp_max));
-            o2[c] = __float_as_uint(rf_scale_pow2(s2 * __uint_as_float(o2[c]), vexp_max));
-          }
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(rf_scale_pow2(f * __uint_as_float(o[c]), vexp_max));
         } else {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o1[c] = o2[c] = 0u;
+          for (int c = 0; c < 32; ++c) o[c] = 0u;
         }
-        if (live) {
-          if constexpr (kTrain) {
-            float4* m1 = reinterpret_cast<float4*>(a.maps + off + c0);
-            float4* m2 = reinterpret_cast<float4*>(a.maps + map2 + off + c0);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              m1[c] = make_float4(__uint_as_float(o1[4 * c]), __uint_as_float(o1[4 * c + 1]),
-                                  __uint_as_float(o1[4 * c + 2]), __uint_as_float(o1[4 * c + 3]));
-              m2[c] = make_float4(__uint_as_float(o2[4 * c]), __uint_as_float(o2[4 * c + 1]),
-                                  __uint_as_float(o2[4 * c + 2]), __uint_as_float(o2[4 * c + 3]));
-            }
-          }
-          uint4* d4 = reinterpret_cast<uint4*>(a.o_r + off + c0);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int e = 8 * c + 2 * i;
-              p[i] = rf_pack2<kBf16>(fmaf(-lam, __uint_as_float(o2[e]), __uint_as_float(o1[e])),
-                                     fmaf(-lam, __uint_as_float(o2[e + 1]), __uint_as_float(o1[e + 1])));
-            }
-            d4[c] = make_uint4(p[0], p[1], p[2], p[3]);
-          }
-        }
+        for (int c = 0; c < 8; ++c)
+          sts128(parts + (uint32_t)w * (RF_BLOCK * D * 4) + part_off<D>(r, c0 / 4 + c), o + 4 * c);
       }
       if constexpr (kTrain) {
-        if (live)
-          a.lse[((size_t)w * g.n1 + n) * a.rows_total + lrow + rr] = have ? m_run + log2f(l_run) : INFINITY;
+        if (r < q_rows)
+          a.lse[((size_t)w * g.n1 + n) * a.rows_total + lrow + q_r0 + r] = have ? m_run + log2f(l_run) : INFINITY;
+      }
+      softmax_bar_sync();
+#pragma unroll 4
+      for (int i = threadIdx.x; i < q_rows * (D / 4); i += 256) {
+        const int row = i / (D / 4), c = i % (D / 4);
+        const float4 o1 = lds128(parts + part_off<D>(row, c));
+        const float4 o2 = lds128(parts + RF_BLOCK * D * 4 + part_off<D>(row, c));
+        const size_t off = rf_row_offset(g, s, g.n1, n, q_r0 + row) + 4 * c;
+        if constexpr (kTrain) {
+          *reinterpret_cast<float4*>(a.maps + off) = o1;
+          *reinterpret_cast<float4*>(a.maps + map2 + off) = o2;
+        }
+        *reinterpret_cast<uint2*>(a.o_r + off) =
+            make_uint2(rf_pack2<kBf16>(fmaf(-lam, o2.x, o1.x), fmaf(-lam, o2.y, o1.y)),
+                       rf_pack2<kBf16>(fmaf(-lam, o2.z, o1.z), fmaf(-lam, o2.w, o1.w)));
       }
     } else {
-      // group w leaves O_w where the tiles were: every product is complete, and so is
-      // every copy (that of Q is waited for where no product did)
-      if (nv == 0) {
-        volatile int no_abort = 0;
-        warp_wait(rf_smem_u32(&sm.bar_q), 0, &no_abort);
-      }
+      // group w leaves its O_w there
       if (!have) sm.row_l[w][r] = 0.f;
-      const uint32_t buf = rf_smem_u32(sm.q) + (uint32_t)w * (RF_BLOCK * D * 4);
+      const uint32_t buf = parts + (uint32_t)w * (RF_BLOCK * D * 4);
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) store_part<D, 32>(buf, ocol + c0, have, r, c0);
     }
@@ -571,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this CTA merges rows [rank, rank + 1) * 128 / size: first each part's factor
       // 2^(m_k - m) / l per row and map (where the V exponents were), then the parts
       const int rows = RF_BLOCK / size;
-      const uint32_t buf = rf_smem_u32(sm.q), am = rf_smem_u32(&sm.row_m[0][0]), al = rf_smem_u32(&sm.row_l[0][0]);
+      const uint32_t buf = parts, am = rf_smem_u32(&sm.row_m[0][0]), al = rf_smem_u32(&sm.row_l[0][0]);
       float* fac = reinterpret_cast<float*>(sm.vexp);  // [size][2][rows]
       if (threadIdx.x < 2 * rows) {
         const int x = threadIdx.x / rows, lr = threadIdx.x - x * rows, row = rank * rows + lr;

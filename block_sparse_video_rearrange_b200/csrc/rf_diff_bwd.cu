@@ -261,13 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t* row = a.sel_idx + row_id * g.max_kv;
   const int num_raw = a.sel_num[row_id];
   const int num = num_raw < 0 ? 0 : (num_raw > g.max_kv ? g.max_kv : num_raw);
+  const uint32_t expired = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT);
   for (int c = threadIdx.x; c < g.max_kv; c += kThreads) sm.list[c] = row[c];
   __syncthreads();
   if (warp == 0) {
     int bad = 0;  // counted by the forward pass and the preparation
     const int cnt = compact_ascending(sm.list, num, nblk, lane, &bad);
     if (lane == 0) {
-      const bool stopped = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT) != 0;
+      const bool stopped = expired != 0;
       sm.first = cnt * rank / size;
       sm.n_valid = stopped ? 0 : cnt * (rank + 1) / size - sm.first;
     }
