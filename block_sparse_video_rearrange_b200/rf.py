@@ -421,48 +421,67 @@ def _device_of(*tensors) -> int:
     return dev
 
 
+# The current stream's handle without a Stream object (which takes longer to make than a kernel to launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:  # pragma: no cover - another torch
+    def _raw_stream(dev: int) -> int:
+        return torch.cuda.current_stream(dev).cuda_stream
+
+
 def _call(where: str, dev: int, stream, *args) -> None:
     """Run a librf entry point with `dev` current, on `stream` or the device's current stream."""
     fn = getattr(_lib, where)
     if torch.cuda.current_device() == dev:
-        st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
-        status = fn(*args, st)
-        if status != RF_OK:
-            _check(status, where)
+        status = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(dev):
-            st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
-            _check(fn(*args, st), where)
+            status = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    if status != RF_OK:
+        _check(status, where)
+
+
+def _need(t: torch.Tensor, shape, dtype: torch.dtype, dev: int, name: str) -> int:
+    """The pointer of a contiguous tensor of this shape and type on CUDA device `dev`."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}; the call's tensors are on "
+                         + (f"cuda:{dev}" if dev >= 0 else "the host, and librf takes CUDA tensors"))
+    if not t.is_contiguous():
+        raise ValueError("librf takes contiguous tensors")
+    return t.data_ptr()
 
 
 def _bytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _lambda_vectors(vecs, outs=()) -> Tuple[int, int, int]:
-    a = vecs[0]
+def _lambda_vectors(a, *others) -> Tuple[int, int, int, int, list]:
+    """Device, dtype code, rows, dim and pointers of lambda's vectors (and their gradients)."""
     if a.dim() != 2 or a.dtype not in DTYPE_CODES:
         raise ValueError(f"lambda's vectors: expected [heads or 1, dim] in bf16, fp16 or fp32, got {tuple(a.shape)} {a.dtype}")
-    for t in (*vecs[1:], *outs):
-        _expect(t, a.shape, a.dtype, "lambda's vectors")
-    return DTYPE_CODES[a.dtype], a.shape[0], a.shape[1]
+    dev, shape, dt = a.get_device(), a.shape, a.dtype
+    if dev < 0:
+        raise ValueError("librf takes CUDA tensors")
+    return (dev, DTYPE_CODES[dt], shape[0], shape[1],
+            [_need(t, shape, dt, dev, "lambda's vectors") for t in (a, *others)])
 
 
 def diff_lambda(a, b, c, d, lambda_init: float, lam, stream=None) -> None:
     """lam[n] = exp(a[n] . b[n]) - exp(c[n] . d[n]) + lambda_init, fp32 [heads]; the vectors are
     [heads, dim], or [1, dim] shared by every head."""
-    dt, rows, dim = _lambda_vectors((a, b, c, d))
-    _expect(lam, (lam.numel(),), torch.float32, "lam")
-    _call("rf_diff_lambda", _device_of(a, b, c, d, lam), stream, _ptr(a), _ptr(b), _ptr(c), _ptr(d), dt, rows, dim,
-          lam.numel(), float(lambda_init), _ptr(lam))
+    dev, dt, rows, dim, vec = _lambda_vectors(a, b, c, d)
+    heads = lam.numel()
+    p = _need(lam, (heads,), torch.float32, dev, "lam")
+    _call("rf_diff_lambda", dev, stream, *vec, dt, rows, dim, heads, float(lambda_init), p)
 
 
 def diff_lambda_backward(a, b, c, d, dlam, da, db, dc, dd, stream=None) -> None:
     """Gradients of lambda's vectors from dlam (fp32 [heads])."""
-    dt, rows, dim = _lambda_vectors((a, b, c, d), (da, db, dc, dd))
-    _expect(dlam, (dlam.numel(),), torch.float32, "dlam")
-    _call("rf_diff_lambda_backward", _device_of(a, b, c, d, dlam, da, db, dc, dd), stream, _ptr(a), _ptr(b), _ptr(c),
-          _ptr(d), dt, rows, dim, dlam.numel(), _ptr(dlam), _ptr(da), _ptr(db), _ptr(dc), _ptr(dd))
+    dev, dt, rows, dim, vec = _lambda_vectors(a, b, c, d, da, db, dc, dd)
+    heads = dlam.numel()
+    p = _need(dlam, (heads,), torch.float32, dev, "dlam")
+    _call("rf_diff_lambda_backward", dev, stream, *vec[:4], dt, rows, dim, heads, p, *vec[4:])
 
 
 def diff_attn_workspace_bytes(plan: Plan, backward: bool = False) -> int:
@@ -487,24 +506,12 @@ def _diff_shapes(plan: Plan):
     return sh
 
 
-def _diff_args(plan: Plan, ws, **tensors):
-    """Check every tensor (None allowed for maps and lse) and return their device and pointers."""
-    shapes, dev, ptrs = _diff_shapes(plan), ws.get_device(), {}
-    for nm, t in tensors.items():
-        if t is None:
-            ptrs[nm] = None
-            continue
-        shape, dt = shapes[nm]
-        if t.shape != shape or t.dtype != dt:
-            raise ValueError(f"{nm}: expected {tuple(shape)} {dt}, got {tuple(t.shape)} {t.dtype}")
-        if not t.is_cuda or t.get_device() != dev:
-            raise ValueError(f"{nm} is on {t.device}, the workspace on {ws.device}")
-        if not t.is_contiguous():
-            raise ValueError("librf takes contiguous tensors")
-        ptrs[nm] = t.data_ptr()
-    if not ws.is_cuda:
-        raise ValueError("librf takes CUDA tensors")
-    return dev, ptrs
+def _diff_ptrs(plan: Plan, dev: int, names, tensors) -> list:
+    shapes = _diff_shapes(plan)
+    return [_need(t, *shapes[nm], dev, nm) for nm, t in zip(names, tensors)]
+
+
+_ATTN_IN = ("q_r", "k_r", "v_r", "select_idx", "select_num", "lam")
 
 
 def diff_attn(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, scale: float, o_r, ws, maps=None, lse=None,
@@ -512,10 +519,11 @@ def diff_attn(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, scale: flo
     """(softmax(scale Q_1 K_1^T) - lam softmax(scale Q_2 K_2^T)) V over the selected blocks, the maps'
     Q and K being the two halves of each head's columns (rearranged order).  maps and lse (both or
     neither) receive what diff_attn_backward needs."""
-    dev, p = _diff_args(plan, ws, q_r=q_r, k_r=k_r, v_r=v_r, select_idx=select_idx, select_num=select_num, lam=lam, o_r=o_r,
-                        maps=maps, lse=lse)
-    _call("rf_diff_attn", dev, stream, plan.handle, p["q_r"], p["k_r"], p["v_r"], p["select_idx"], p["select_num"], p["lam"],
-          float(scale), p["o_r"], p["maps"], p["lse"], _ptr(ws), _bytes(ws))
+    dev = q_r.get_device()
+    p = _diff_ptrs(plan, dev, _ATTN_IN, (q_r, k_r, v_r, select_idx, select_num, lam))
+    o, w = _diff_ptrs(plan, dev, ("o_r",), (o_r,))[0], _need(ws, ws.shape, ws.dtype, dev, "ws")
+    kept = [None if t is None else _need(t, *_diff_shapes(plan)[nm], dev, nm) for nm, t in (("maps", maps), ("lse", lse))]
+    _call("rf_diff_attn", dev, stream, plan.handle, *p, float(scale), o, *kept, w, _bytes(ws))
 
 
 def diff_attn_backward(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, scale: float, maps, lse, do_r, dq_r, dk_r,
@@ -523,11 +531,12 @@ def diff_attn_backward(plan: Plan, q_r, k_r, v_r, select_idx, select_num, lam, s
     """Gradients of diff_attn from do_r and what it kept (maps, lse); rearranged order."""
     if maps is None or lse is None:
         raise ValueError("the backward pass needs the maps and lse that diff_attn kept")
-    dev, p = _diff_args(plan, ws, q_r=q_r, k_r=k_r, v_r=v_r, select_idx=select_idx, select_num=select_num, lam=lam, maps=maps,
-                        lse=lse, do_r=do_r, dq_r=dq_r, dk_r=dk_r, dv_r=dv_r, dlam=dlam)
-    _call("rf_diff_attn_backward", dev, stream, plan.handle, p["q_r"], p["k_r"], p["v_r"], p["select_idx"], p["select_num"],
-          p["lam"], float(scale), p["maps"], p["lse"], p["do_r"], p["dq_r"], p["dk_r"], p["dv_r"], p["dlam"], _ptr(ws),
-          _bytes(ws))
+    dev = q_r.get_device()
+    p = _diff_ptrs(plan, dev, _ATTN_IN, (q_r, k_r, v_r, select_idx, select_num, lam))
+    more = _diff_ptrs(plan, dev, ("maps", "lse", "do_r", "dq_r", "dk_r", "dv_r", "dlam"),
+                      (maps, lse, do_r, dq_r, dk_r, dv_r, dlam))
+    w = _need(ws, ws.shape, ws.dtype, dev, "ws")
+    _call("rf_diff_attn_backward", dev, stream, plan.handle, *p, float(scale), *more, w, _bytes(ws))
 
 
 def rearrange_rows(plan: Plan, x, y, inverse: bool = False, stream=None) -> None:
@@ -558,12 +567,12 @@ class DiffBuffers:
 
 
 def _norm_strides(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
-    if t.dim() != 4:
+    st = t.stride()
+    if len(st) != 4:
         raise ValueError(f"{name}: expected [batch, rows, groups, width], got {tuple(t.shape)}")
-    sb, sr, sg, sc = t.stride()
-    if sc != 1 and t.shape[3] > 1 and t.numel():
+    if st[3] != 1 and t.shape[3] > 1 and t.numel():
         raise ValueError(f"{name}: the channels of a group must be contiguous")
-    return sb, sr, sg
+    return st[:3]
 
 
 def _norm_desc(x, span: str, act: str, eps: float, param_dtype=torch.float32, y=None) -> NormDesc:
@@ -575,8 +584,7 @@ def _norm_desc(x, span: str, act: str, eps: float, param_dtype=torch.float32, y=
         raise ValueError(f"group norm takes bf16, fp16 or fp32, got {x.dtype} and {param_dtype}")
     xs = _norm_strides(x, "x")
     ys = xs if y is None else _norm_strides(y, "y")
-    return NormDesc(x.shape[0], x.shape[1], x.shape[2], x.shape[3], *xs, *ys, DTYPE_CODES[x.dtype],
-                    DTYPE_CODES[param_dtype], SPANS[span], ACTS[act], float(eps))
+    return NormDesc(*x.shape, *xs, *ys, DTYPE_CODES[x.dtype], DTYPE_CODES[param_dtype], SPANS[span], ACTS[act], float(eps))
 
 
 def group_norm_workspace(x, span: str = "row") -> torch.Tensor:
@@ -592,11 +600,22 @@ def group_norm_stats(x, span: str = "row") -> Optional[torch.Tensor]:
     return torch.empty((x.shape[0], x.shape[2], 2), dtype=torch.float32, device=x.device) if span == "sample" else None
 
 
-def _norm_params(x, *params) -> torch.dtype:
+def _norm_tensors(x, like, params) -> Tuple[int, torch.dtype, list]:
+    """Device, parameter type and pointers of the parameters; `like`: tensors of x's shape and type."""
+    dev, shape, dt = x.get_device(), x.shape, x.dtype
+    if dev < 0:
+        raise ValueError("librf takes CUDA tensors")
+    for nm, t in like:
+        if t.shape != shape or t.dtype != dt or t.get_device() != dev:
+            raise ValueError(f"{nm}: expected {tuple(shape)} {dt} on {x.device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
     pdt = params[0].dtype
-    for t in params:
-        _expect(t, (x.shape[2], x.shape[3]), pdt, "gamma, beta and their gradients")
-    return pdt
+    if len(shape) != 4:
+        raise ValueError(f"x: expected [batch, rows, groups, width], got {tuple(shape)}")
+    return dev, pdt, [_need(t, shape[2:], pdt, dev, "gamma, beta and their gradients") for t in params]
+
+
+def _norm_kept(x, stats, dev: int) -> int:
+    return _need(stats, (x.shape[0], x.shape[2], 2), torch.float32, dev, "stats")
 
 
 def group_norm(x, gamma, beta, y, span: str = "row", act: str = "none", eps: float = 1e-5, stats=None, ws=None,
@@ -604,39 +623,35 @@ def group_norm(x, gamma, beta, y, span: str = "row", act: str = "none", eps: flo
     """y = act(gamma (x - mu) / sqrt(var + eps) + beta) of x [batch, rows, groups, width], mu and var over a group's
     channels of each row (span "row") or of all rows of a batch element ("sample").  gamma, beta: [groups, width].
     Span "sample" takes ws (group_norm_workspace) and keeps stats (group_norm_stats) for the backward pass."""
-    _expect(y, x.shape, x.dtype, "y")
-    desc = _norm_desc(x, span, act, eps, _norm_params(x, gamma, beta), y)
+    dev, pdt, (g, b) = _norm_tensors(x, (("y", y),), (gamma, beta))
+    desc = _norm_desc(x, span, act, eps, pdt, y)
+    kept = w = None
     if span == "sample":
         if ws is None:
             ws = group_norm_workspace(x, span)
         if stats is None:
             stats = group_norm_stats(x, span)
-        _expect(stats, (x.shape[0], x.shape[2], 2), torch.float32, "stats")
-    else:
-        stats = None
-    _call("rf_group_norm", _device_of(x, gamma, beta, y, stats, ws), stream, ctypes.byref(desc), x.data_ptr(), _ptr(gamma),
-          _ptr(beta), y.data_ptr(), _ptr(stats), _ptr(ws), _bytes(ws))
+        kept, w = _norm_kept(x, stats, dev), _need(ws, ws.shape, ws.dtype, dev, "ws")
+    _call("rf_group_norm", dev, stream, ctypes.byref(desc), x.data_ptr(), g, b, y.data_ptr(), kept, w,
+          0 if w is None else _bytes(ws))
 
 
 def group_norm_backward(x, gamma, beta, dy, stats, dx, dgamma, dbeta, span: str = "row", act: str = "none",
                         eps: float = 1e-5, ws=None, stream=None) -> None:
     """Gradients of group_norm; stats as it kept them (None with span "row")."""
-    _expect(dy, x.shape, x.dtype, "dy")
-    _expect(dx, x.shape, x.dtype, "dx")
-    desc = _norm_desc(x, span, act, eps, _norm_params(x, gamma, beta, dgamma, dbeta), dy)
-    if _norm_strides(dx, "dx") != _norm_strides(x, "x"):
+    dev, pdt, (g, b, dg, db) = _norm_tensors(x, (("dy", dy), ("dx", dx)), (gamma, beta, dgamma, dbeta))
+    desc = _norm_desc(x, span, act, eps, pdt, dy)
+    if dx.stride() != x.stride():
         raise ValueError("dx must have x's strides")
+    kept = None
     if span == "sample":
         if stats is None:
             raise ValueError("span sample needs the stats that group_norm kept")
-        _expect(stats, (x.shape[0], x.shape[2], 2), torch.float32, "stats")
-    else:
-        stats = None
+        kept = _norm_kept(x, stats, dev)
     if ws is None:
         ws = group_norm_workspace(x, span)
-    _call("rf_group_norm_backward", _device_of(x, gamma, beta, dy, stats, dx, dgamma, dbeta, ws), stream,
-          ctypes.byref(desc), x.data_ptr(), _ptr(gamma), _ptr(beta), dy.data_ptr(), _ptr(stats), dx.data_ptr(),
-          _ptr(dgamma), _ptr(dbeta), _ptr(ws), _bytes(ws))
+    _call("rf_group_norm_backward", dev, stream, ctypes.byref(desc), x.data_ptr(), g, b, dy.data_ptr(), kept,
+          dx.data_ptr(), dg, db, _need(ws, ws.shape, ws.dtype, dev, "ws"), _bytes(ws))
 
 
 _PIPELINES = {}        # host pipelines (with their device buffers) of recent problem shapes
