@@ -293,6 +293,12 @@ __device__ __forceinline__ float cluster_ld(uint32_t addr) {
   return v;
 }
 
+// Overlapped launches: lets the next kernel of the stream (launched as a
+// dependent) start where this one leaves room; and, in that kernel, waits until
+// the one before it is complete and its writes are visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Orders this thread's plain shared-memory stores before later accesses by the
 // asynchronous units (TMA, tcgen05).
 __device__ __forceinline__ void fence_async_smem() {

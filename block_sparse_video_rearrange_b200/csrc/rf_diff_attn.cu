@@ -130,6 +130,12 @@ __device__ __forceinline__ void quarter_exp(const uint32_t* sr, int c0, int vr, 
   const uint64_t sl2x2 = rf_f2(__float_as_uint(sl2), __float_as_uint(sl2));
   const uint64_t negm2 = rf_f2(__float_as_uint(neg_m), __float_as_uint(neg_m));
   uint32_t pk[16];
+  if (!kFull && c0 >= vr) {  // nothing valid here (uniform over the CTA)
+#pragma unroll
+    for (int c = 0; c < 16; ++c) pk[c] = 0u;
+    tmem_st16(p_addr, pk);
+    return;
+  }
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     float x0, x1;
@@ -152,6 +158,13 @@ __device__ __forceinline__ void quarter_exp_fine(const uint32_t* sr, int c0, int
   const uint64_t sl2x2 = rf_f2(__float_as_uint(sl2), __float_as_uint(sl2));
   const uint64_t negm2 = rf_f2(__float_as_uint(neg_m), __float_as_uint(neg_m));
   uint32_t pk[16], lo[16];
+  if (c0 >= vr) {  // nothing valid here (uniform over the CTA)
+#pragma unroll
+    for (int c = 0; c < 16; ++c) pk[c] = 0u;
+    tmem_st16(p_addr, pk);
+    tmem_st16(p_addr + 32, pk);
+    return;
+  }
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     float x0, x1;
@@ -255,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float lam = a.lambda[n];
   const uint32_t expired = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT);
   for (int c = threadIdx.x; c < g.max_kv; c += kThreads) sm.list[c] = row[c];
+  wait_for_previous();  // the copies of V and their exponents
   for (int c = threadIdx.x; c < nblk; c += kThreads) sm.vexp[c] = ve[c];
   const int num = num_raw < 0 ? 0 : (num_raw > g.max_kv ? g.max_kv : num_raw);
   __syncthreads();
@@ -520,8 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // row's own thread, 16 bytes here and there, the two fp32 maps took 11,000
       // cycles a CTA (now 2,000).
       const float f = have ? 1.0f / l_run : 0.f;
+      const int cols = (warp & 3) * 32 < q_rows ? D : 0;  // none of a warp without rows
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
+      for (int c0 = 0; c0 < cols; c0 += 32) {
         uint32_t o[32];
         if (have) {
           tmem_ld32(ocol + c0, o);

@@ -22,7 +22,9 @@
 //                            it, in ascending order.
 //   rf_diff_dlam_kernel      sums dlambda's parts in block order.
 // Two passes (S and dA computed in both, 7 matrix products for 5) need no
-// atomic additions, so the gradients are the same bits every time.
+// atomic additions, so the gradients are the same bits every time.  dQ does not
+// need dK and dV and is launched as their kernel's dependent, into the SMs that
+// its last wave leaves free.
 //
 // A and dS are rounded once, to the inputs' type, for the tensor cores.  fp16
 // has no room for their range, so there A and dS carry a power of two chosen
@@ -451,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(rf_smem_u32(&sm.bar_ds_full[t & 1]));
     }
     if (!ok) record_timeout(abort, a.status, 7);
+    wait_for_previous();  // dK and dV are complete when this kernel is
     const bool have = nv > 0 && !*abort && warp_wait(rf_smem_u32(&sm.bar_final), 0, abort) && !*abort;
     if (have) tc_fence_after();
     constexpr int kN = D / 4;  // columns each warpgroup writes
@@ -523,6 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int size = (int)cluster_size(), rank = (int)cluster_rank();  // CTAs sharing these items
   rf_cta_item(g, a.order, g.n2, blockIdx.x / size, gk, tb);
   const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
+  wait_for_previous();
+  if (threadIdx.x == 0) launch_dependents();  // dQ reads nothing of this kernel: it may fill the last wave
   const int group = g.n1 / g.n2;
   int k_r0, k_rows;
   rf_block_span(s, tb - s.qblk_off, k_r0, k_rows);

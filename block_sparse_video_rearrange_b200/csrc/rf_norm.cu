@@ -802,6 +802,7 @@ rf_status_t rf_group_norm(const rf_norm_desc_t* d, const void* x, const void* ga
   const bool sample = d->span == RF_NORM_SAMPLE;
   if (d->batch == 0 || d->rows == 0) return RF_OK;
   if (!x || !y || (sample && !stats)) return rf_fail(RF_ERR_INVALID_ARG, "null tensor");
+  if (reinterpret_cast<uintptr_t>(stats) & 7) return rf_fail(RF_ERR_INVALID_ARG, "stats must be 8-byte aligned");
   if (x == y) return rf_fail(RF_ERR_INVALID_ARG, "y aliases x");
   if (!disjoint(d, d->y_stride_b, d->y_stride_r, d->y_stride_g))
     return rf_fail(RF_ERR_INVALID_ARG, "elements of y overlap (a broadcast output)");
@@ -828,6 +829,7 @@ rf_status_t rf_group_norm_backward(const rf_norm_desc_t* d, const void* x, const
     return RF_OK;
   }
   if (!x || !dy || !dx || (sample && !stats)) return rf_fail(RF_ERR_INVALID_ARG, "null tensor");
+  if (reinterpret_cast<uintptr_t>(stats) & 7) return rf_fail(RF_ERR_INVALID_ARG, "stats must be 8-byte aligned");
   if (dx == x || dx == dy) return rf_fail(RF_ERR_INVALID_ARG, "dx aliases an input");
   if (!disjoint(d, d->x_stride_b, d->x_stride_r, d->x_stride_g))
     return rf_fail(RF_ERR_INVALID_ARG, "elements of dx overlap (x is broadcast)");

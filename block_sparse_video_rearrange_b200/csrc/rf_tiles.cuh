@@ -169,7 +169,10 @@ inline rf_status_t rf_prepare_kernel(size_t smem, const char* what, int* regs = 
   return RF_OK;
 }
 
-// Launches `kern` with `size` CTAs per cluster for each of `items`.
+// Launches `kern` with `size` CTAs per cluster for each of `items`, as a dependent of
+// the stream's kernel before it: it may start before that one ends and must call
+// wait_for_previous() before it touches what that one writes, and in any case
+// before it ends.
 template <class... Args>
 inline rf_status_t rf_launch_split(void (*kern)(Args...), long long items, int size, int threads, size_t smem,
                                    cudaStream_t st, const char* what, Args... args) {
@@ -179,13 +182,15 @@ inline rf_status_t rf_launch_split(void (*kern)(Args...), long long items, int s
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)size;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)size;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = size > 1 ? 1 : 0;
+  cfg.numAttrs = size > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return rf_check_launch(what);
   return rf_check_launch(what);
 }

@@ -555,7 +555,8 @@ class DiffBuffers:
         f32 = dict(dtype=torch.float32, device=device)
         self.o_r = torch.empty(shp_q, dtype=dt, device=device)
         self.lam = torch.empty(plan.n1, **f32)
-        self.ws = torch.zeros(diff_attn_workspace_bytes(plan, train) // 4 + 64, dtype=torch.int32, device=device)
+        self.ws = torch.empty(diff_attn_workspace_bytes(plan, train) // 4 + 64, dtype=torch.int32, device=device)
+        self.ws[:64] = 0                 # the status words; every other region is written before it is read
         self.maps = self.lse = None
         if train:
             self.maps = torch.empty((2, *shp_q), **f32)

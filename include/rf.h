@@ -427,7 +427,8 @@ RF_API rf_status_t rf_plan_permutation(const rf_plan_t* plan, int32_t seq, int64
  * Shapes, layouts, rearrangement, selection (the ranking's q . k is the sum of
  * both maps' scores) and the inverse are those of a plan with the same heads;
  * scale is typically 1 / sqrt(d / 2).  Native precision and blockShape 128 x 128
- * (RF_ERR_UNSUPPORTED otherwise). */
+ * (RF_ERR_UNSUPPORTED otherwise).  Kernel attributes are set once per device: after
+ * cudaDeviceReset these calls must not be used on that device again. */
 
 /* lambda[n] = exp(a[n] . b[n]) - exp(c[n] . d[n]) + lambda_init.
  * a, b, c, d  : the learned vectors, contiguous [vec_heads, dim] of dtype (bf16,
@@ -510,7 +511,7 @@ typedef struct {
 } rf_norm_desc_t;
 /* Workspace of both calls (host only). */
 RF_API rf_status_t rf_group_norm_workspace_bytes(const rf_norm_desc_t* desc, int64_t* out);
-/* stats: RF_NORM_SAMPLE: fp32 [batch, groups, 2], receives {mu, 1 / sqrt(var +
+/* stats: RF_NORM_SAMPLE: fp32 [batch, groups, 2] (8-byte aligned), receives {mu, 1 / sqrt(var +
  * eps)}, which the backward pass reads; RF_NORM_ROW: may be NULL (and so may ws).
  * Outputs must not overlap inputs, nor (by zero or small strides) themselves. */
 RF_API rf_status_t rf_group_norm(const rf_norm_desc_t* desc, const void* x, const void* gamma,

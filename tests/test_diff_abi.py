@@ -118,7 +118,7 @@ def test_norm_descriptor_refusals(kw, status):
 
 
 @pytest.mark.parametrize("kw,change", [
-    ({}, dict(x=None)), ({}, dict(gamma=None)), ({}, dict(stats=None)), ({}, dict(y=FAKE[0])), ({}, dict(ws=None)),
+    ({}, dict(x=None)), ({}, dict(gamma=None)), ({}, dict(stats=None)), ({}, dict(stats=ctypes.c_void_p((5 << 20) + 4))), ({}, dict(y=FAKE[0])), ({}, dict(ws=None)),
     (dict(y_stride_b=0), {}), (dict(y_stride_r=47), {}), (dict(y_stride_g=0), {}),
 ])
 def test_norm_call_refusals(kw, change):
