@@ -645,3 +645,26 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(uint32_t fmt, uint32_t m, 
          | (b_mn_major << 16)  // B major
          | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+
+// Launches `kern` as a dependent of the stream's kernel before it: it is set up
+// while that one runs (about 1 us less between two short kernels) and starts with
+// wait_for_previous().
+template <class... Args>
+inline rf_status_t rf_launch_dependent(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t st, const char* what,
+                                       Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return rf_check_launch(what);
+  return rf_check_launch(what);
+}

@@ -97,6 +97,7 @@ __device__ __forceinline__ void lambda_exps(const LambdaArgs& x, int row, int la
 // One warp per vector row; a row shared by every head writes every lambda.
 // Latency-bound: a few kilobytes, one launch.
 __global__ void __launch_bounds__(128) rf_diff_lambda_kernel(const __grid_constant__ LambdaArgs x, float* lambda) {
+  wait_for_previous();
   const int row = (int)((blockIdx.x * 128 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (row >= x.vec_heads) return;
   float e1, e2;
@@ -112,8 +113,9 @@ __global__ void __launch_bounds__(128) rf_diff_lambda_kernel(const __grid_consta
 // d lambda / d a = e1 b and so on; vectors shared by every head take the sum of
 // dlambda over the heads (in a fixed order).
 __global__ void __launch_bounds__(128)
-    rf_diff_lambda_bwd_kernel(const __grid_constant__ LambdaArgs x, const float* __restrict__ dlambda, void* da,
+    rf_diff_lambda_bwd_kernel(const __grid_constant__ LambdaArgs x, const float* dlambda, void* da,
                               void* db, void* dc, void* dd) {
+  wait_for_previous();
   const int row = (int)((blockIdx.x * 128 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (row >= x.vec_heads) return;
   float g = 0.f;
@@ -163,8 +165,8 @@ rf_status_t rf_diff_lambda(const void* a, const void* b, const void* c, const vo
   if (!lambda) return rf_fail(RF_ERR_INVALID_ARG, "null lambda");
   if ((st = rf_require_device()) != RF_OK) return st;
   const LambdaArgs x{a, b, c, d, dtype, vec_heads, dim, heads, lambda_init};
-  rf_diff_lambda_kernel<<<(unsigned)((vec_heads + 3) / 4), 128, 0, (cudaStream_t)stream>>>(x, lambda);
-  return rf_check_launch("rf_diff_lambda_kernel");
+  return rf_launch_dependent(rf_diff_lambda_kernel, dim3((unsigned)((vec_heads + 3) / 4)), 128, (cudaStream_t)stream,
+                             "rf_diff_lambda_kernel", x, lambda);
 }
 
 rf_status_t rf_diff_lambda_backward(const void* a, const void* b, const void* c, const void* d, rf_dtype_t dtype,
@@ -176,9 +178,8 @@ rf_status_t rf_diff_lambda_backward(const void* a, const void* b, const void* c,
   if (!dlambda || !da || !db || !dc || !dd) return rf_fail(RF_ERR_INVALID_ARG, "null gradient");
   if ((st = rf_require_device()) != RF_OK) return st;
   const LambdaArgs x{a, b, c, d, dtype, vec_heads, dim, heads, 0.f};
-  rf_diff_lambda_bwd_kernel<<<(unsigned)((vec_heads + 3) / 4), 128, 0, (cudaStream_t)stream>>>(x, dlambda, da, db, dc,
-                                                                                             dd);
-  return rf_check_launch("rf_diff_lambda_bwd_kernel");
+  return rf_launch_dependent(rf_diff_lambda_bwd_kernel, dim3((unsigned)((vec_heads + 3) / 4)), 128, (cudaStream_t)stream,
+                             "rf_diff_lambda_bwd_kernel", x, dlambda, da, db, dc, dd);
 }
 
 rf_status_t rf_diff_attn_workspace_bytes(const rf_plan_t* p, int32_t backward, int64_t* out) {

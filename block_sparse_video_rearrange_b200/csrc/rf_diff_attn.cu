@@ -262,13 +262,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const size_t row_id = (size_t)tb * g.n1 + n;
   const int32_t* row = a.sel_idx + row_id * g.max_kv;
+  wait_for_previous();  // the copies of V and their exponents, and what came before them
   // The whole row, its length and every block's exponent at once: one round trip.
   const int32_t* ve = a.v_exp + (size_t)gk * g.t_qblk + s.qblk_off;
   const int num_raw = a.sel_num[row_id];
   const float lam = a.lambda[n];
   const uint32_t expired = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT);
   for (int c = threadIdx.x; c < g.max_kv; c += kThreads) sm.list[c] = row[c];
-  wait_for_previous();  // the copies of V and their exponents
   for (int c = threadIdx.x; c < nblk; c += kThreads) sm.vexp[c] = ve[c];
   const int num = num_raw < 0 ? 0 : (num_raw > g.max_kv ? g.max_kv : num_raw);
   __syncthreads();
@@ -664,11 +664,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the attention it serves.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(256) rf_diff_prep_v_kernel(const __grid_constant__ RfGeomDev g,
-                                                             const uint16_t* __restrict__ v,
-                                                             uint4* __restrict__ v16,
-                                                             int32_t* __restrict__ v_exp) {
+                                                             const uint16_t* v, uint4* v16, int32_t* v_exp) {
   constexpr int kChunks = RF_BLOCK * D / 8 / 256;  // 16-byte chunks per thread
   __shared__ uint32_t top_w[8];
+  wait_for_previous();
   const int head = blockIdx.x / g.t_qblk, tb = blockIdx.x % g.t_qblk;
   const RfSeqDev& s = g.seq[rf_seq_of_qblk(g, tb)];
   int r0, nrows;
@@ -773,14 +772,9 @@ rf_status_t rf_launch_diff_attn(const rf_plan* p, const void* q_r, const void* k
   uint4* v16 = reinterpret_cast<uint4*>(w + lay.v16);
   int32_t* ve = reinterpret_cast<int32_t*>(w + lay.v_exp);
   const unsigned vgrid = (unsigned)((long long)g.t_qblk * g.n2);
-  if (g.d == 128) {
-    if (bf) rf_diff_prep_v_kernel<128, true><<<vgrid, 256, 0, st>>>(g, v, v16, ve);
-    else    rf_diff_prep_v_kernel<128, false><<<vgrid, 256, 0, st>>>(g, v, v16, ve);
-  } else {
-    if (bf) rf_diff_prep_v_kernel<64, true><<<vgrid, 256, 0, st>>>(g, v, v16, ve);
-    else    rf_diff_prep_v_kernel<64, false><<<vgrid, 256, 0, st>>>(g, v, v16, ve);
-  }
-  if ((s = rf_check_launch("rf_diff_prep_v_kernel")) != RF_OK) return s;
+  auto prep = g.d == 128 ? (bf ? rf_diff_prep_v_kernel<128, true> : rf_diff_prep_v_kernel<128, false>)
+                         : (bf ? rf_diff_prep_v_kernel<64, true> : rf_diff_prep_v_kernel<64, false>);
+  if ((s = rf_launch_dependent(prep, dim3(vgrid), 256, st, "rf_diff_prep_v_kernel", g, v, v16, ve)) != RF_OK) return s;
   DiffArgs a;
   a.g = g;
   a.order = rf_order(g);

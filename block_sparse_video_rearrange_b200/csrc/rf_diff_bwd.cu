@@ -896,12 +896,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // (CTAs past t_qblk * n1 read V).  HBM-bound: 10 D bytes per row and head.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(256)
-    rf_diff_prep_bwd_kernel(const __grid_constant__ RfGeomDev g, const int32_t* __restrict__ sel_idx,
-                            const int32_t* __restrict__ sel_num, const float* __restrict__ lambda,
-                            const uint16_t* __restrict__ d_o, const uint16_t* __restrict__ v,
-                            const float* __restrict__ maps, const float* __restrict__ lse, long long rows_total,
-                            int words, float* __restrict__ stats, uint32_t* __restrict__ bits,
-                            float* __restrict__ dlam, uint32_t* __restrict__ amax, uint32_t* __restrict__ status) {
+    rf_diff_prep_bwd_kernel(const __grid_constant__ RfGeomDev g, const int32_t* sel_idx,
+                            const int32_t* sel_num, const float* lambda,
+                            const uint16_t* d_o, const uint16_t* v,
+                            const float* maps, const float* lse, long long rows_total,
+                            int words, float* stats, uint32_t* bits,
+                            float* dlam, uint32_t* amax, uint32_t* status) {
+  wait_for_previous();
   __shared__ int list[RF_MAX_KV_LIST];
   __shared__ float part[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -999,8 +1000,8 @@ __global__ void __launch_bounds__(256)
 }
 
 // dlambda[n] = -sum over the query blocks of their sums of delta_2, in a fixed order.
-__global__ void __launch_bounds__(256) rf_diff_dlam_kernel(const float* __restrict__ part, int t_qblk,
-                                                           float* __restrict__ dlambda) {
+__global__ void __launch_bounds__(256) rf_diff_dlam_kernel(const float* part, int t_qblk, float* dlambda) {
+  wait_for_previous();
   __shared__ float red[8];
   float sum = 0.f;
   for (int i = threadIdx.x; i < t_qblk; i += 256) sum += part[(size_t)blockIdx.x * t_qblk + i];
@@ -1043,12 +1044,14 @@ rf_status_t launch_t(const rf_plan* p, const BwdArgs& a, const void* q_r, const 
   if (cudaMemsetAsync(bits, 0, (size_t)((char*)amax - (char*)bits) + 256, st) != cudaSuccess)
     return rf_check_launch("cudaMemsetAsync(rf_diff backward)");
   const unsigned prep = (unsigned)(gq + (kBf16 ? 0 : gkv));
-  rf_diff_prep_bwd_kernel<D, kBf16><<<prep, 256, 0, st>>>(
-      g, a.sel_idx, a.sel_num, a.lambda, static_cast<const uint16_t*>(do_r), static_cast<const uint16_t*>(v_r), maps,
-      lse, p->rows_total, a.words, stats, bits, dlam_part, amax, a.status);
-  if ((s = rf_check_launch("rf_diff_prep_bwd_kernel")) != RF_OK) return s;
-  rf_diff_dlam_kernel<<<(unsigned)g.n1, 256, 0, st>>>(dlam_part, g.t_qblk, dlambda);
-  if ((s = rf_check_launch("rf_diff_dlam_kernel")) != RF_OK) return s;
+  if ((s = rf_launch_dependent(rf_diff_prep_bwd_kernel<D, kBf16>, dim3(prep), 256, st, "rf_diff_prep_bwd_kernel", g,
+                               a.sel_idx, a.sel_num, a.lambda, static_cast<const uint16_t*>(do_r),
+                               static_cast<const uint16_t*>(v_r), maps, lse, (long long)p->rows_total, a.words, stats, bits,
+                               dlam_part, amax, a.status)) != RF_OK)
+    return s;
+  if ((s = rf_launch_dependent(rf_diff_dlam_kernel, dim3((unsigned)g.n1), 256, st, "rf_diff_dlam_kernel",
+                               (const float*)dlam_part, g.t_qblk, dlambda)) != RF_OK)
+    return s;
   if ((s = rf_launch_split(kkv, gkv, rf_split(g, g.n2, g.n1 / g.n2), kThreads, skv, st, "rf_diff_dkv_kernel", mq[1],
                            mk[0], mv[0], mo[1], a)) != RF_OK)
     return s;

@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, VEC * NV <= 8 ? (kBwd ? 3 : 4) : 1)
   T* out = static_cast<T*>(a.y) + (kBwd ? g * a.xs_g : g * a.ys_g) + lane * VEC;
   // channels in pairs for the paired fp32 instructions (a lone channel beside a zero)
   constexpr int P = (E + 1) / 2;
+  wait_for_previous();
   uint64_t gm[P], bt[P], sg[kBwd ? P : 1], sb[kBwd ? P : 1];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
@@ -381,6 +382,7 @@ __device__ __forceinline__ long long chan_off(long long c, int width, long long 
 template <class T, int VEC, bool kBwd>
 __global__ void __launch_bounds__(kThreads) rf_norm_partial_kernel(const __grid_constant__ NormArgs a, int tile) {
   __shared__ float red[2][kThreads][VEC];
+  wait_for_previous();
   const int b = blockIdx.z;
   const long long ch = (long long)a.groups * a.width;
   const int lanes = kThreads / tile, rl = threadIdx.x / tile;
@@ -492,6 +494,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 template <bool kBwd>
 __global__ void __launch_bounds__(kReduceThreads) rf_norm_stats_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float red[kReduceThreads / 32];
+  wait_for_previous();
   const int b = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
   const long long ch = (long long)a.groups * a.width;
   const float* w = a.ws + (long long)b * a.slices * 2 * ch + (long long)g * a.width;
@@ -528,11 +531,12 @@ __global__ void __launch_bounds__(kReduceThreads) rf_norm_stats_kernel(const __g
 }
 
 // dgamma and dbeta: the partial sums [parts][2][channels] added in a fixed order.
-__global__ void __launch_bounds__(kReduceThreads) rf_norm_params_kernel(const float* __restrict__ ws, int parts,
+__global__ void __launch_bounds__(kReduceThreads) rf_norm_params_kernel(const float* ws, int parts,
                                                                         long long ch, int gamma_first, int pdt,
                                                                         void* dgamma, void* dbeta) {
   // 32 channels per block, 32 lanes of parts, merged in order
   __shared__ float red[2][32][33];
+  wait_for_previous();
   const int cl = threadIdx.x & 31, pl = threadIdx.x >> 5;
   const long long c = (long long)blockIdx.x * 32 + cl;
   float s0 = 0.f, s1 = 0.f;
@@ -563,6 +567,7 @@ __global__ void __launch_bounds__(kReduceThreads) rf_norm_params_kernel(const fl
 // y (or dx) of every element from the statistics.
 template <class T, int VEC, bool kBwd>
 __global__ void __launch_bounds__(kThreads) rf_norm_apply_kernel(const __grid_constant__ NormArgs a, int tile) {
+  wait_for_previous();
   const int b = blockIdx.z;
   const long long ch = (long long)a.groups * a.width;
   const int lanes = kThreads / tile, rl = threadIdx.x / tile;
@@ -707,8 +712,9 @@ NormArgs make_args(const rf_norm_desc_t* d, const void* x, const void* gamma, co
 }
 
 template <class T, int VEC, int NV, bool kBwd>
-void row_launch(const NormArgs& a, int lanes, cudaStream_t st) {
-  rf_norm_row_kernel<T, VEC, NV, kBwd><<<dim3((unsigned)a.slices, (unsigned)a.groups), kThreads, 0, st>>>(a, lanes);
+rf_status_t row_launch(const NormArgs& a, int lanes, cudaStream_t st) {
+  return rf_launch_dependent(rf_norm_row_kernel<T, VEC, NV, kBwd>, dim3((unsigned)a.slices, (unsigned)a.groups), kThreads,
+                             st, "rf_norm_row_kernel", a, lanes);
 }
 
 template <class T, bool kBwd>
@@ -719,15 +725,13 @@ rf_status_t run_rows(const NormArgs& a, bool vec, cudaStream_t st) {
   while (lanes < 32 && lanes < units) lanes <<= 1;
   const int nv = (units + lanes - 1) / lanes;
   if (vec) {
-    if (nv <= 1)      row_launch<T, V, 1, kBwd>(a, lanes, st);
-    else if (nv <= 2) row_launch<T, V, 2, kBwd>(a, lanes, st);
-    else              row_launch<T, V, 8, kBwd>(a, lanes, st);
-  } else {
-    if (nv <= 1)      row_launch<T, 1, 1, kBwd>(a, lanes, st);
-    else if (nv <= 4) row_launch<T, 1, 4, kBwd>(a, lanes, st);
-    else              row_launch<T, 1, 32, kBwd>(a, lanes, st);
+    if (nv <= 1) return row_launch<T, V, 1, kBwd>(a, lanes, st);
+    if (nv <= 2) return row_launch<T, V, 2, kBwd>(a, lanes, st);
+    return row_launch<T, V, 8, kBwd>(a, lanes, st);
   }
-  return rf_check_launch("rf_norm_row_kernel");
+  if (nv <= 1) return row_launch<T, 1, 1, kBwd>(a, lanes, st);
+  if (nv <= 4) return row_launch<T, 1, 4, kBwd>(a, lanes, st);
+  return row_launch<T, 1, 32, kBwd>(a, lanes, st);
 }
 
 // Channel vectors of a block: all of them up to 256, so that a row is read in
@@ -743,16 +747,17 @@ rf_status_t run_samples_v(const NormArgs& a, cudaStream_t st) {
   const long long cv = ((long long)a.groups * a.width + VEC - 1) / VEC;
   const unsigned tiles = (unsigned)((cv + tile - 1) / tile);
   if (tiles > 65535u) return rf_fail(RF_ERR_UNSUPPORTED, "too many channels");
-  rf_norm_partial_kernel<T, VEC, kBwd><<<dim3((unsigned)a.slices, tiles, (unsigned)a.batch), kThreads, 0, st>>>(a, tile);
-  rf_status_t s = rf_check_launch("rf_norm_partial_kernel");
+  rf_status_t s = rf_launch_dependent(rf_norm_partial_kernel<T, VEC, kBwd>, dim3((unsigned)a.slices, tiles, (unsigned)a.batch),
+                                      kThreads, st, "rf_norm_partial_kernel", a, tile);
   if (s != RF_OK) return s;
-  rf_norm_stats_kernel<kBwd><<<(unsigned)(a.batch * a.groups), kReduceThreads, 0, st>>>(a);
-  if ((s = rf_check_launch("rf_norm_stats_kernel")) != RF_OK) return s;
+  s = rf_launch_dependent(rf_norm_stats_kernel<kBwd>, dim3((unsigned)(a.batch * a.groups)), kReduceThreads, st,
+                          "rf_norm_stats_kernel", a);
+  if (s != RF_OK) return s;
   const long long lanes = kThreads / tile;
   const long long most = (a.rows + lanes - 1) / lanes, want = std::max<long long>(1, 148ll * 4 / ((long long)tiles * a.batch));
   const unsigned gx = (unsigned)std::max<long long>(1, std::min(most, want));
-  rf_norm_apply_kernel<T, VEC, kBwd><<<dim3(gx, tiles, (unsigned)a.batch), kThreads, 0, st>>>(a, tile);
-  return rf_check_launch("rf_norm_apply_kernel");
+  return rf_launch_dependent(rf_norm_apply_kernel<T, VEC, kBwd>, dim3(gx, tiles, (unsigned)a.batch), kThreads, st,
+                             "rf_norm_apply_kernel", a, tile);
 }
 
 template <class T, bool kBwd>
@@ -837,9 +842,9 @@ rf_status_t rf_group_norm_backward(const rf_norm_desc_t* d, const void* x, const
   if ((st = rf_require_device()) != RF_OK) return st;
   const NormArgs a = make_args(d, x, gamma, beta, dy, dx, const_cast<float*>(stats), ws, true);
   if ((st = run<true>(d, a, (cudaStream_t)stream)) != RF_OK) return st;
-  rf_norm_params_kernel<<<(unsigned)((ch + 31) / 32), kReduceThreads, 0, (cudaStream_t)stream>>>(
-      a.ws, sample ? a.batch * a.slices : a.slices, ch, sample ? 0 : 1, a.pdt, dgamma, dbeta);
-  return rf_check_launch("rf_norm_params_kernel");
+  return rf_launch_dependent(rf_norm_params_kernel, dim3((unsigned)((ch + 31) / 32)), kReduceThreads, (cudaStream_t)stream,
+                             "rf_norm_params_kernel", (const float*)a.ws, sample ? a.batch * a.slices : a.slices,
+                             (long long)ch, sample ? 0 : 1, a.pdt, dgamma, dbeta);
 }
 
 }  // extern "C"
