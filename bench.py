@@ -100,7 +100,7 @@ def load_peaks():
 
 def kernel_sha(name="rf_attn.cu"):
     h = hashlib.sha256()
-    for n in (name, "rf_device.cuh"):
+    for n in (name, "rf_device.cuh", "rf_tiles.cuh"):
         with open(os.path.join(ROOT, "block_sparse_video_rearrange_b200", "csrc", n), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]

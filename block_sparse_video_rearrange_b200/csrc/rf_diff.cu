@@ -6,6 +6,7 @@
 #include <cmath>
 #include <string>
 
+#include "rf_async.cuh"
 #include "rf_device.cuh"
 
 RfDiffLayout rf_diff_layout(const rf_plan* p) {

@@ -43,7 +43,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "rf_async.cuh"
 #include "rf_device.cuh"
+#include "rf_lists.cuh"
 #include "rf_tiles.cuh"
 
 namespace {

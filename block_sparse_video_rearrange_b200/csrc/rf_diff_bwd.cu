@@ -33,7 +33,9 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
+#include "rf_async.cuh"
 #include "rf_device.cuh"
+#include "rf_lists.cuh"
 #include "rf_tiles.cuh"
 
 namespace {
@@ -788,64 +790,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_pin16(da);
       tc_fence_before();
       mbar_arrive(rf_smem_u32(&sm.bar_read));
-      auto exps = [&](uint32_t* x, uint32_t nl) {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          uint64_t l0, l1;
-          lds_2x2(nl + 4 * i, l0, l1);
-          uint64_t y0 = rf_fma2(rf_f2(x[i], x[i + 1]), sl, l0), y1 = rf_fma2(rf_f2(x[i + 2], x[i + 3]), sl, l1);
-          if constexpr (!kBf16) {
-            y0 = rf_add2(y0, ua);
-            y1 = rf_add2(y1, ua);
-          }
-          float f0, f1, f2, f3;
-          rf_f2_split(y0, f0, f1);
-          rf_f2_split(y1, f2, f3);
-          x[i] = __float_as_uint(rf_ex2(f0));
-          x[i + 1] = __float_as_uint(rf_ex2(f1));
-          x[i + 2] = __float_as_uint(rf_ex2(f2));
-          x[i + 3] = __float_as_uint(rf_ex2(f3));
-        }
-      };
-      exps(s1, num);
-      exps(s2, num + 256);
+      // All of a column group's work together: the exponentials of one group run
+      // under the arithmetic of another.
       const float nlam = -lds_f(rf_smem_u32(&sm.lam[0]) + 4u * st);
-      const uint64_t nl2 = rf_f2(__float_as_uint(nlam), __float_as_uint(nlam));
-      uint32_t out[16];  // A in [0, 8) for now; dS_2 in [0, 8) and dS_1 in [8, 16)
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const uint64_t p2 = rf_mul2(nl2, rf_f2(s2[i], s2[i + 1]));
-        float a0, a1;
-        rf_f2_split(rf_add2(rf_f2(s1[i], s1[i + 1]), p2), a0, a1);
-        out[i >> 1] = rf_pack2<kBf16>(a0, a1);
-        rf_f2_split(p2, a0, a1);
-        s2[i] = __float_as_uint(a0);
-        s2[i + 1] = __float_as_uint(a1);
-      }
-      sts128(a_c0 + (t & 1) * (RF_BLOCK * 128), out);
-      sts128(a_c1 + (t & 1) * (RF_BLOCK * 128), out + 4);
-      fence_async_smem();
+      const uint64_t nl = rf_f2(__float_as_uint(nlam), __float_as_uint(nlam));
+      uint32_t out_a[8], out[16];  // A; dS_2 in [0, 8) and dS_1 in [8, 16)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
-        uint64_t d1[2], d2[2];
+        uint64_t l1[2], l2[2], d1[2], d2[2];
+        lds_2x2(num + 4 * i, l1[0], l1[1]);
+        lds_2x2(num + 256 + 4 * i, l2[0], l2[1]);
         lds_2x2(num + 512 + 4 * i, d1[0], d1[1]);
         lds_2x2(num + 768 + 4 * i, d2[0], d2[1]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int c = i + 2 * k;
+          uint64_t x = rf_fma2(rf_f2(s1[c], s1[c + 1]), sl, l1[k]), y = rf_fma2(rf_f2(s2[c], s2[c + 1]), sl, l2[k]);
+          if constexpr (!kBf16) {
+            x = rf_add2(x, ua);
+            y = rf_add2(y, ua);
+          }
+          float f0, f1;
+          rf_f2_split(x, f0, f1);
+          const uint64_t p1 = rf_f2(__float_as_uint(rf_ex2(f0)), __float_as_uint(rf_ex2(f1)));
+          rf_f2_split(y, f0, f1);
+          const uint64_t p2 = rf_mul2(nl, rf_f2(__float_as_uint(rf_ex2(f0)), __float_as_uint(rf_ex2(f1))));
+          rf_f2_split(rf_add2(p1, p2), f0, f1);
+          out_a[c >> 1] = rf_pack2<kBf16>(f0, f1);
           const uint64_t dd = rf_f2(da[c], da[c + 1]);
           uint64_t t1 = rf_fma2(d1[k], neg1, dd), t2 = rf_fma2(d2[k], neg1, dd);
           if constexpr (!kBf16) {
             t1 = rf_mul2(t1, us);
             t2 = rf_mul2(t2, us);
           }
-          float y0, y1;
-          rf_f2_split(rf_mul2(rf_f2(s1[c], s1[c + 1]), t1), y0, y1);
-          out[8 + (c >> 1)] = rf_pack2<kBf16>(y0, y1);
-          rf_f2_split(rf_mul2(rf_f2(s2[c], s2[c + 1]), t2), y0, y1);
-          out[c >> 1] = rf_pack2<kBf16>(y0, y1);
+          rf_f2_split(rf_mul2(p1, t1), f0, f1);
+          out[8 + (c >> 1)] = rf_pack2<kBf16>(f0, f1);
+          rf_f2_split(rf_mul2(p2, t2), f0, f1);
+          out[c >> 1] = rf_pack2<kBf16>(f0, f1);
         }
       }
+      sts128(a_c0 + (t & 1) * (RF_BLOCK * 128), out_a);
+      sts128(a_c1 + (t & 1) * (RF_BLOCK * 128), out_a + 4);
+      fence_async_smem();
       tmem_st16(s2c, out);
       tmem_wait_st();
       tc_fence_before();

@@ -26,6 +26,7 @@
 #include <string>
 #include <utility>
 
+#include "rf_async.cuh"
 #include "rf_device.cuh"
 
 namespace {
