@@ -114,10 +114,10 @@ struct __align__(1024) DkvSmem {
   float stats[kKvStages][4][64];
   float lam[kKvStages];
   uint64_t bar_kv, bar_aux;
-  uint64_t bar_full[kKvStages];  // step t's tiles landed, and A's buffer and dS's slot free (products of t - 2)
+  uint64_t bar_full[kKvStages];  // step t's tiles landed, A's buffer and dS's slot free (products of t - 2), and
+                                 // S_1, S_2 and dA of t - 1 read into registers
   uint64_t bar_empty[kKvStages];
   uint64_t bar_sd_full;  // S_1, S_2 and dA of a step computed, the rows' numbers there
-  uint64_t bar_read;     // and read into registers
   uint64_t bar_ew[2];    // A, dS_1, dS_2 of a step stored, by parity
   uint64_t bar_final, bar_drain;
   uint32_t tmem_base;
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float nlse1 = str[0], nlse2 = str[64], dc1 = c1 * str[128], dc2 = c2 * str[192];
     bool ok = true;
     for (int t = 0; t < 2 * nv; ++t) {
-      if (!warp_wait(rf_smem_u32(&sm.bar_sd_full[t & 1]), (t >> 1) & 1, abort)) { ok = false; break; }
+      if (!warp_wait<true>(rf_smem_u32(&sm.bar_sd_full[t & 1]), (t >> 1) & 1, abort)) { ok = false; break; }
       tc_fence_after();
       const uint32_t base = lane_base + 192 * (t & 1) + 16 * e;
       // valid keys of this thread's 16 (all of them but in the partial prefix block)
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // through shared memory (two buffers).  So a step's elements hardly ever wait for
 // its products, and the warpgroups drift apart until one's exponentials run under
 // another's arithmetic.  A barrier check costs its warp 100 to 200 cycles, so
-// there are few: one per step for a computing thread, three for the issuing warp.
+// there are few: one per step for a computing thread, two for the issuing warp.
 // Warpgroup e takes queries [16 e, +16) of the step, which is one 16-wide slice
 // of the reduction of dV and dK.
 // Rows that a query block does not have carry -lse = -inf (P = 0); their Q and
@@ -544,11 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(rf_smem_u32(&sm.bar_kv), 1);
     mbar_init(rf_smem_u32(&sm.bar_aux), 1);
     for (int i = 0; i < kKvStages; ++i) {
-      mbar_init(rf_smem_u32(&sm.bar_full[i]), 2);
+      mbar_init(rf_smem_u32(&sm.bar_full[i]), 2 + kCompute);
       mbar_init(rf_smem_u32(&sm.bar_empty[i]), 1);
     }
     mbar_init(rf_smem_u32(&sm.bar_sd_full), 2);  // the products' commit, and the issuing warp itself
-    mbar_init(rf_smem_u32(&sm.bar_read), kCompute);
     mbar_init(rf_smem_u32(&sm.bar_ew[0]), kCompute);
     mbar_init(rf_smem_u32(&sm.bar_ew[1]), kCompute);
     mbar_init(rf_smem_u32(&sm.bar_final), 1);
@@ -716,8 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int t = 0; ok && t < nt; ++t) {
         if (t + 1 < nt) {
-          if (!warp_wait<true>(rf_smem_u32(&sm.bar_full[(t + 1) % kKvStages]), ((t + 1) / kKvStages) & 1, abort) ||
-              !warp_wait<true>(rf_smem_u32(&sm.bar_read), t & 1, abort)) {
+          if (!warp_wait<true>(rf_smem_u32(&sm.bar_full[(t + 1) % kKvStages]), ((t + 1) / kKvStages) & 1, abort)) {
             ok = false;
             break;
           }
@@ -770,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t a_row = rf_smem_u32(sm.a[0]) + 128u * r;
     const uint32_t a_c0 = a_row + 16u * ((2 * e) ^ (r & 7)), a_c1 = a_row + 16u * ((2 * e + 1) ^ (r & 7));
     bool ok = true;
+    if (ni > 0) mbar_arrive(rf_smem_u32(&sm.bar_full[0]));  // nothing to read before the first step
     for (int t = 0; t < 2 * ni; ++t) {
       const uint32_t sh = 4 * (t & 3);
       const uint32_t s1c = lane_base + 64u * ((0x2130u >> sh) & 15u) + 16 * e;
@@ -778,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int st = t % kKvStages;
       // this thread's 16 queries' numbers: -lse_1, -lse_2, delta_1, delta_2, 256 bytes apart
       const uint32_t num = stats0 + (uint32_t)st * kStatBytes;
-      if (!warp_wait(rf_smem_u32(&sm.bar_sd_full), t & 1, abort)) { ok = false; break; }
+      if (!warp_wait<true>(rf_smem_u32(&sm.bar_sd_full), t & 1, abort)) { ok = false; break; }
       tc_fence_after();
       uint32_t s1[16], s2[16], da[16];
       tmem_ld16(s1c, s1);
@@ -789,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_pin16(s2);
       tmem_pin16(da);
       tc_fence_before();
-      mbar_arrive(rf_smem_u32(&sm.bar_read));
+      mbar_arrive(rf_smem_u32(&sm.bar_full[(t + 1) % kKvStages]));
       // All of a column group's work together: the exponentials of one group run
       // under the arithmetic of another.
       const float nlam = -lds_f(rf_smem_u32(&sm.lam[0]) + 4u * st);
