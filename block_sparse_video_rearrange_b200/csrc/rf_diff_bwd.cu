@@ -210,7 +210,7 @@ __device__ __forceinline__ void merge_rows(uint32_t buf, int size, int rank, int
 // issuing warp that a step's tiles have landed and that its columns are free.
 // Bound: per 128 x 128 block the tensor pipe about 2,300 cycles (an N = 64
 // product with both operands in shared memory takes 54 cycles, 35 with A in
-// TMEM, 32 by its arithmetic); the ex2 unit 2,048.  Measured: about 3,400 (2.68 ms
+// TMEM, 32 by its arithmetic); the ex2 unit 2,048.  Measured: about 3,500 (2.70 ms
 // for 5 heads of the (21, 30, 52) grid with 512 text rows at s = 0.8; 3.04 ms with
 // one map per warpgroup, a barrier each for K, V and dQ, and 128-row stages).
 template <int D, bool kBf16>
@@ -504,11 +504,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Rows that a query block does not have carry -lse = -inf (P = 0); their Q and
 // dO rows are zeroed in shared memory, so that nothing infinite meets that 0.
 // Bound: per 128 x 128 block and head the tensor pipe about 2,800 cycles (S and dA
-// at N = 64, see above), the ex2 unit 2,048.  Measured: about 4,700 (3.57 ms on the
+// at N = 64, see above), the ex2 unit 2,048.  Measured: about 4,400 (3.31 ms on the
 // layer above; 5.57 ms when a step's products waited for A and dS of the one
-// before).  The issuing warp and the computing threads are both busy nearly all
-// of that time; 128-query steps, whose products are fed faster, do not fit: S_1,
-// S_2 and dA beside dV and dK would take 640 TMEM columns of 512.
+// before, 3.57 ms with the exponentials of all columns before the rest).  The
+// issuing warp and the computing threads are both busy nearly all of that time;
+// 128-query steps, whose products are fed faster, do not fit: S_1, S_2 and dA
+// beside dV and dK would take 640 TMEM columns of 512.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     rf_diff_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

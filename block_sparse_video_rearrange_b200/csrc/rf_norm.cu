@@ -18,7 +18,7 @@
 // fits).  Measured (bf16): rows of 20 x 128, 33,272 of them: 71 us, 4.8 TB/s;
 // 16,640 of them with SiLU, forward and backward: 46 and 83 us (the instructions of
 // the activation's derivative, not the memory, set the latter); samples of 16,128
-// x 320, two of them, with SiLU: 22 us in three launches.
+// x 320, two of them, with SiLU: 22 us in three dependent launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -728,7 +728,7 @@ rf_status_t run_rows(const NormArgs& a, bool vec, cudaStream_t st) {
   if (vec) {
     if (nv <= 1) return row_launch<T, V, 1, kBwd>(a, lanes, st);
     if (nv <= 2) return row_launch<T, V, 2, kBwd>(a, lanes, st);
-    return row_launch<T, V, 8, kBwd>(a, lanes, st);
+    return row_launch<T, V, sizeof(T) == 4 ? 8 : 4, kBwd>(a, lanes, st);  // 1,024 channels
   }
   if (nv <= 1) return row_launch<T, 1, 1, kBwd>(a, lanes, st);
   if (nv <= 4) return row_launch<T, 1, 4, kBwd>(a, lanes, st);
