@@ -139,6 +139,16 @@ def rainfusion_diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         return torch.cat(parts)
 
 
+def _overlaps(x: torch.Tensor) -> bool:
+    """Whether elements of x may share memory (broadcast rows, sliding windows): its gradient needs its own layout."""
+    reach = 1
+    for st, n in sorted((st, n) for st, n in zip(x.stride(), x.shape) if n > 1):
+        if st < reach:
+            return True
+        reach += (n - 1) * st
+    return False
+
+
 class _GroupNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gamma, beta, span, act, eps, train):
@@ -186,8 +196,8 @@ def group_norm(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, num_gro
         raise ValueError(f"x: expected [batch, rows, channels] or [batch, rows, groups, width], got {tuple(shape)}")
     if not x.is_cuda:
         raise ValueError("group_norm takes CUDA tensors")
-    if x.stride(3) != 1 or any(n > 1 and st == 0 for n, st in zip(x.shape, x.stride())):
-        x = x.contiguous()               # broadcast rows, or channels that are not neighbours
+    if x.stride(3) != 1 or _overlaps(x):
+        x = x.contiguous()               # rows that share memory, or channels that are not neighbours
     gw = (x.shape[2], x.shape[3])
     gamma, beta = gamma.reshape(gw).contiguous(), beta.reshape(gw).contiguous()
     with torch.cuda.device(x.device):

@@ -156,3 +156,10 @@ def test_python_refuses_host_tensors_and_wrong_shapes():
     q = torch.zeros(1, 4, 128, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         diff.rainfusion_diff_attention(q, q, q, [(128, 0, 0, 0)], v)
+
+
+def test_which_layouts_share_memory():
+    from block_sparse_video_rearrange_b200.diff import _overlaps
+    x = torch.zeros(2, 3, 4, 8)
+    assert not any(_overlaps(v) for v in (x, x.transpose(1, 2), x[:, :, 1:, :5], x[:, ::2], x[:1, :1, :1, :1], x[:, :0]))
+    assert _overlaps(x[:1].expand(2, 3, 4, 8)) and _overlaps(torch.zeros(64).unfold(0, 16, 8))

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from block_sparse_video_rearrange_b200 import rf
+from block_sparse_video_rearrange_b200 import diff, rf
 
 pytestmark = pytest.mark.gpu
 
@@ -205,3 +205,21 @@ def test_many_rows_past_32_bit_offsets():
         rf.group_norm(x, gamma, beta, y, span=span)
         rf.group_norm(x.contiguous(), gamma, beta, z, span=span)
         assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("span", ["row", "sample"])
+def test_windows_that_share_memory(span):
+    """Sliding windows over one buffer: the gradient is that of a copy of the windows, added up."""
+    gen = torch.Generator().manual_seed(5)
+    base = torch.randn(8 * 41, generator=gen).cuda()
+    gamma, beta = (torch.randn(16, generator=gen).cuda() for _ in range(2))
+    up = torch.randn(1, 40, 16, generator=gen).cuda()
+    got = []
+    for copied in (False, True):
+        leaf = base.clone().requires_grad_()
+        x = leaf.unfold(0, 16, 8)[None]
+        y = diff.group_norm(x.clone(memory_format=torch.contiguous_format) if copied else x, gamma, beta, 2, span=span, act="silu")
+        y.backward(up)
+        got.append((y.detach(), leaf.grad))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
