@@ -615,6 +615,16 @@ def _norm_tensors(x, like, params) -> Tuple[int, torch.dtype, list]:
     return dev, pdt, [_need(t, shape[2:], pdt, dev, "gamma, beta and their gradients") for t in params]
 
 
+def _made_on(stream, dev: int):
+    """The context in which a call makes its own temporaries: their memory belongs to the stream that the kernels run
+    on, so what is allocated after the call returns cannot take it before they are done."""
+    if stream is None:
+        return torch.cuda.stream(None)
+    if not isinstance(stream, torch.cuda.Stream):     # a raw handle, or another library's stream object
+        stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
 def _norm_kept(x, stats, dev: int) -> int:
     return _need(stats, (x.shape[0], x.shape[2], 2), torch.float32, dev, "stats")
 
@@ -623,15 +633,16 @@ def group_norm(x, gamma, beta, y, span: str = "row", act: str = "none", eps: flo
                stream=None) -> None:
     """y = act(gamma (x - mu) / sqrt(var + eps) + beta) of x [batch, rows, groups, width], mu and var over a group's
     channels of each row (span "row") or of all rows of a batch element ("sample").  gamma, beta: [groups, width].
-    Span "sample" takes ws (group_norm_workspace) and keeps stats (group_norm_stats) for the backward pass."""
+    Span "sample" takes ws (group_norm_workspace) and keeps stats (group_norm_stats) for the backward pass; without
+    them the call makes its own, on the stream that it runs on."""
     dev, pdt, (g, b) = _norm_tensors(x, (("y", y),), (gamma, beta))
     desc = _norm_desc(x, span, act, eps, pdt, y)
     kept = w = None
     if span == "sample":
-        if ws is None:
-            ws = group_norm_workspace(x, span)
-        if stats is None:
-            stats = group_norm_stats(x, span)
+        if ws is None or stats is None:
+            with _made_on(stream, dev):
+                ws = group_norm_workspace(x, span) if ws is None else ws
+                stats = group_norm_stats(x, span) if stats is None else stats
         kept, w = _norm_kept(x, stats, dev), _need(ws, ws.shape, ws.dtype, dev, "ws")
     _call("rf_group_norm", dev, stream, ctypes.byref(desc), x.data_ptr(), g, b, y.data_ptr(), kept, w,
           0 if w is None else _bytes(ws))
@@ -650,7 +661,8 @@ def group_norm_backward(x, gamma, beta, dy, stats, dx, dgamma, dbeta, span: str 
             raise ValueError("span sample needs the stats that group_norm kept")
         kept = _norm_kept(x, stats, dev)
     if ws is None:
-        ws = group_norm_workspace(x, span)
+        with _made_on(stream, dev):
+            ws = group_norm_workspace(x, span)
     _call("rf_group_norm_backward", dev, stream, ctypes.byref(desc), x.data_ptr(), g, b, dy.data_ptr(), kept,
           dx.data_ptr(), dg, db, _need(ws, ws.shape, ws.dtype, dev, "ws"), _bytes(ws))
 
