@@ -26,8 +26,11 @@ RfDiffLayout rf_diff_layout(const rf_plan* p) {
   l.stats = l.end_serve;
   l.bits = up(l.stats + (int64_t)g.n1 * qb * 4 * RF_BLOCK * 4);
   l.dlam = up(l.bits + (int64_t)g.n1 * qb * l.words * 4);
-  l.amax = up(l.dlam + (int64_t)g.n1 * qb * 4);
-  l.end = l.amax + 256;
+  l.do_row = up(l.dlam + (int64_t)g.n1 * qb * 4);
+  const bool f16 = p->dtype == RF_FP16;
+  l.do_blk = up(l.do_row + (f16 ? (int64_t)g.n1 * qb * RF_BLOCK * 4 : 0));
+  l.v_blk = up(l.do_blk + (f16 ? (int64_t)g.n1 * qb * 8 : 0));
+  l.end = up(l.v_blk + (f16 ? (int64_t)g.n2 * qb * 4 : 0));
   return l;
 }
 

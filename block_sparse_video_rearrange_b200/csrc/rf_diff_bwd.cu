@@ -27,9 +27,12 @@
 // its last wave leaves free.
 //
 // A and dS are rounded once, to the inputs' type, for the tensor cores.  fp16
-// has no room for their range, so there A and dS carry a power of two chosen
-// from the tensors' largest |dO|, |V| and |lambda| (exact to undo): the bound
-// on |dS| lands at 2^15, values down to 2^-29 of it stay normal.
+// has no room for their range, so there A and dS carry powers of two (exact to
+// undo), one for each accumulation, so that no row's gradient is scaled by what
+// it does not add up.  dQ: one per query row, from its own |dO| and the largest
+// |V| of the blocks it lists.  dK, dV: one per key block, from its own |V| and
+// the |dO|, |delta| and |lambda| of the (head, query block) pairs that list it.
+// The bound on |dS| lands at 2^15; values down to 2^-29 of it stay normal.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -59,7 +62,9 @@ struct BwdArgs {
   const float* lambda;       // [n1]
   const float* stats;        // [n1][t_qblk][2][4][64]: -lse_1, -lse_2, delta_1, delta_2 of 64 rows
   const uint32_t* bits;      // [n1][t_qblk][words]
-  const uint32_t* amax;      // fp16: largest |dO|, |V|, |lambda| as fp32 bits
+  const float* do_row;       // fp16: largest |dO| of a row, [n1][t_qblk][128]
+  const float2* do_blk;      // fp16: {largest |dO|, |delta|} of a block, [n1][t_qblk]
+  const float* v_blk;        // fp16: largest |V| of a block, [n2][t_qblk]
   int words;
   uint16_t* dq;
   uint16_t* dk;
@@ -69,18 +74,15 @@ struct BwdArgs {
   float sl2;                 // scale * log2(e)
 };
 
-// Power-of-two exponents that A and dS carry through the 16-bit rounding.
-template <int D, bool kBf16>
-__device__ __forceinline__ void carry_exponents(const uint32_t* amax, int& ea, int& es) {
-  ea = es = 0;
-  if constexpr (!kBf16) {
-    const float mdo = __uint_as_float(amax[0]), mv = __uint_as_float(amax[1]);
-    const float ml = fmaxf(1.f, __uint_as_float(amax[2]));
-    // |A| <= 1 + |lambda|, |dA|, |delta| <= D max|dO| max|V|
-    ea = max(14 - rf_ceil_log2(ml), -100);
-    const float bound = 2.0f * D * mdo * mv * ml;
-    if (bound > 0.f && bound < INFINITY) es = min(max(15 - rf_ceil_log2(bound), -100), 100);
-  }
+// fp16: the power-of-two exponents that A (|A| <= 1 + |lambda| <= 2 ml) and dS (at
+// most `bound`) carry through the 16-bit rounding.
+__device__ __forceinline__ float lambda_size(float lambda) {
+  const float l = fabsf(lambda);
+  return l < INFINITY ? fmaxf(1.f, l) : 1.f;
+}
+__device__ __forceinline__ int carry_a(float ml) { return max(14 - rf_ceil_log2(ml), -100); }
+__device__ __forceinline__ int carry_ds(float bound) {
+  return bound > 0.f && bound < INFINITY ? min(max(15 - rf_ceil_log2(bound), -100), 100) : 0;
 }
 
 template <int D>
@@ -100,6 +102,8 @@ struct __align__(1024) DqSmem {
   int abort;
   int n_valid;
   int first;  // this CTA's part of the list begins here
+  uint32_t v_max;            // fp16: largest |V| of the listed blocks, as fp32 bits
+  float f_row[RF_BLOCK];     // what a row of the accumulated dQ is multiplied by
   int list[RF_MAX_KV_LIST];
 };
 
@@ -123,6 +127,7 @@ struct __align__(1024) DkvSmem {
   uint32_t tmem_base;
   int abort;
   int n_items;
+  uint32_t ds_max, lam_max;  // fp16: bound on |dS| and largest |lambda| (at least 1) over the items, as fp32 bits
 };
 
 // Zeroes rows [nrows, 64) of a 64-row tile's 128-byte-wide boxes (a row is 128
@@ -179,9 +184,9 @@ __device__ __forceinline__ void store_row(uint32_t taddr, bool have, float f, bo
 }
 
 // Rows [rank, rank + 1) * 128 / size of the sum over the cluster's partial
-// [128][D] buffers, times f, to 16 bits; by the 512 computing threads.
-template <int D, bool kBf16, class Row>
-__device__ __forceinline__ void merge_rows(uint32_t buf, int size, int rank, int live_rows, float f, Row row_ptr) {
+// [128][D] buffers, times factor(row), to 16 bits; by the 512 computing threads.
+template <int D, bool kBf16, class Factor, class Row>
+__device__ __forceinline__ void merge_rows(uint32_t buf, int size, int rank, int live_rows, Factor factor, Row row_ptr) {
   const int rows = RF_BLOCK / size;
   for (int i = threadIdx.x; i < rows * (D / 4); i += kCompute) {
     const int row = rank * rows + i / (D / 4), c = i % (D / 4);
@@ -194,6 +199,7 @@ __device__ __forceinline__ void merge_rows(uint32_t buf, int size, int rank, int
       s.z += p.z;
       s.w += p.w;
     }
+    const float f = factor(row);
     *reinterpret_cast<uint2*>(row_ptr(row) + 4 * c) =
         make_uint2(rf_pack2<kBf16>(f * s.x, f * s.y), rf_pack2<kBf16>(f * s.z, f * s.w));
   }
@@ -278,6 +284,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm.first = cnt * rank / size;
       sm.n_valid = stopped ? 0 : cnt * (rank + 1) / size - sm.first;
     }
+    if constexpr (!kBf16) {  // over the whole list: the same in every CTA that shares it
+      const float* vb = a.v_blk + (size_t)gk * g.t_qblk + s.qblk_off;
+      uint32_t top = 0u;
+      for (int c = lane; c < cnt; c += 32) top = max(top, __float_as_uint(vb[sm.list[c]]));
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) sm.v_max = top;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -286,8 +299,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nv = sm.n_valid;
   const int* list = sm.list + sm.first;
   const int vr_last = s.Lp - (s.n_pb - 1) * RF_BLOCK;  // valid rows of the last prefix block
-  int ea, es;
-  carry_exponents<D, kBf16>(a.amax, ea, es);
 
   if (warp >= 16) {
     if (warp == kLoadWarp && nv > 0) {
@@ -427,7 +438,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float* str = a.stats + ((size_t)n * g.t_qblk + tb) * (4 * RF_BLOCK) + (r >> 6) * 256 + (r & 63);
-    const float c1 = kBf16 ? 1.f : rf_pow2(es), c2 = -a.lambda[n] * c1;
+    const float lam = a.lambda[n];
+    int es = 0;  // |dS| <= max(1, |lambda|) (|dA| + |delta|), each of them at most D |dO| |V| of this row and its list
+    if constexpr (!kBf16)
+      es = carry_ds(2.0f * D * __uint_as_float(sm.v_max) * lambda_size(lam) *
+                    a.do_row[((size_t)n * g.t_qblk + tb) * RF_BLOCK + r]);
+    const float c1 = kBf16 ? 1.f : rf_pow2(es), c2 = -lam * c1;
     const float nlse1 = str[0], nlse2 = str[64], dc1 = c1 * str[128], dc2 = c2 * str[192];
     bool ok = true;
     for (int t = 0; t < 2 * nv; ++t) {
@@ -468,8 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // the partial dQ where the tiles were (every copy and product is complete)
       store_part<D, kN>(rf_smem_u32(sm.q), tcol, have, r, col);
+      if (e == 0) sm.f_row[r] = f;
       cluster_sync();
-      merge_rows<D, kBf16>(rf_smem_u32(sm.q), size, rank, q_rows, f,
+      merge_rows<D, kBf16>(rf_smem_u32(sm.q), size, rank, q_rows, [&](int row) { return sm.f_row[row]; },
                            [&](int row) { return a.dq + rf_row_offset(g, s, g.n1, n, q_r0 + row); });
       cluster_sync();  // the others have read this CTA's part
     }
@@ -555,6 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(rf_smem_u32(&sm.bar_drain), 1);
     sm.abort = 0;
     sm.n_items = 0;
+    sm.ds_max = 0u;
+    sm.lam_max = __float_as_uint(1.f);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -564,12 +583,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   // (head of the group, query block) pairs that list this key block
   int mine = 0;
+  float ds_top = 0.f, lam_top = 1.f;
+  const float v_top = kBf16 ? 0.f : D * a.v_blk[(size_t)gk * g.t_qblk + tb];
   for (int i = threadIdx.x; i < group * a.words; i += kThreads) {
-    const int hh = i / a.words;
-    mine += __popc(a.bits[((size_t)(gk * group + hh) * g.t_qblk + tb) * a.words + (i - hh * a.words)]);
+    const int hh = i / a.words, wd = i - hh * a.words, n = gk * group + hh;
+    uint32_t word = a.bits[((size_t)n * g.t_qblk + tb) * a.words + wd];
+    mine += __popc(word);
+    if constexpr (!kBf16) {
+      if (word) {
+        const float ml = lambda_size(a.lambda[n]);
+        const float2* blk = a.do_blk + (size_t)n * g.t_qblk + s.qblk_off + wd * 32;
+        lam_top = fmaxf(lam_top, ml);
+        for (; word; word &= word - 1) {
+          const float2 m = blk[__ffs(word) - 1];
+          ds_top = fmaxf(ds_top, ml * fmaf(v_top, m.x, m.y));  // |dA| + |delta|
+        }
+      }
+    }
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0 && mine) atomicAdd(&sm.n_items, mine);
+  if constexpr (!kBf16) {  // positive numbers order as their bits do
+    const uint32_t dt = __reduce_max_sync(0xffffffffu, __float_as_uint(ds_top));
+    const uint32_t lt = __reduce_max_sync(0xffffffffu, __float_as_uint(lam_top));
+    if (lane == 0) {
+      atomicMax(&sm.ds_max, dt);
+      atomicMax(&sm.lam_max, lt);
+    }
+  }
   const bool stopped = *reinterpret_cast<volatile uint32_t*>(a.status + RF_STATUS_TIMEOUT) != 0;
   tc_fence_before();
   const int any_stopped = __syncthreads_or(stopped ? 1 : 0);
@@ -577,8 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   const int i0 = sm.n_items * rank / size;  // this CTA's items: [i0, i0 + ni)
   const int ni = any_stopped ? 0 : sm.n_items * (rank + 1) / size - i0;
-  int ea, es;
-  carry_exponents<D, kBf16>(a.amax, ea, es);
+  const int ea = kBf16 ? 0 : carry_a(__uint_as_float(sm.lam_max)), es = kBf16 ? 0 : carry_ds(__uint_as_float(sm.ds_max));
 
   if (warp >= 16) {
     if (warp == kLoadWarp && ni > 0) {
@@ -855,9 +895,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       store_part<D, kN>(bv, lane_base + kDv + col, have, r, col);
       store_part<D, kN>(bk, kcol, have, r, col);
       cluster_sync();
-      merge_rows<D, kBf16>(bv, size, rank, k_rows, fv,
+      merge_rows<D, kBf16>(bv, size, rank, k_rows, [&](int) { return fv; },
                            [&](int row) { return a.dv + rf_row_offset(g, s, g.n2, gk, k_r0 + row); });
-      merge_rows<D, kBf16>(bk, size, rank, k_rows, fk,
+      merge_rows<D, kBf16>(bk, size, rank, k_rows, [&](int) { return fk; },
                            [&](int row) { return a.dk + rf_row_offset(g, s, g.n2, gk, k_r0 + row); });
       cluster_sync();  // the others have read this CTA's part
     }
@@ -878,19 +918,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Per (query block, head): packs each row's -lse_1, -lse_2, delta_1 and delta_2
 // (rows the block does not have: -inf, -inf, 0, 0), sums delta_2 over the
 // block's rows in a fixed order, and sets this query block's bit for every key
-// block it lists.  fp16: also the largest finite |dO|, |V| and |lambda|
-// (CTAs past t_qblk * n1 read V).  HBM-bound: 10 D bytes per row and head.
+// block it lists.  fp16: also the largest finite |dO| of each row, |dO| and |delta|
+// of the block, and (CTAs past t_qblk * n1) |V| of each key block.
+// 10 D bytes per row and head.
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, D == 128 && kBf16 ? 8 : 1)
     rf_diff_prep_bwd_kernel(const __grid_constant__ RfGeomDev g, const int32_t* sel_idx,
-                            const int32_t* sel_num, const float* lambda,
-                            const uint16_t* d_o, const uint16_t* v,
+                            const int32_t* sel_num, const uint16_t* d_o, const uint16_t* v,
                             const float* maps, const float* lse, long long rows_total,
                             int words, float* stats, uint32_t* bits,
-                            float* dlam, uint32_t* amax, uint32_t* status) {
+                            float* dlam, float* do_row, float2* do_blk, float* v_blk, uint32_t* status) {
   wait_for_previous();
   __shared__ int list[RF_MAX_KV_LIST];
   __shared__ float part[8];
+  __shared__ float2 part_top[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kPer = D / 32;  // columns per lane
   const bool is_v = (int)blockIdx.x >= g.t_qblk * g.n1;
@@ -901,19 +942,27 @@ __global__ void __launch_bounds__(256)
   int r0, nrows;
   rf_block_span(s, lq, r0, nrows);
   auto decode = [](uint32_t u) { return kBf16 ? __uint_as_float(u << 16) : __half2float(__ushort_as_half((unsigned short)u)); };
-  float top = 0.f;
-  auto finite_max = [&](float x) {
+  float2 top = make_float2(0.f, 0.f);  // of |dO| (or |V|) and |delta|
+  auto finite_max = [](float& t, float x) {
     const float m = fabsf(x);
-    if (m < INFINITY) top = fmaxf(top, m);
+    if (m < INFINITY) t = fmaxf(t, m);
+  };
+  // the largest over the block's warps, by thread 0 (after a barrier)
+  auto block_top = [&]() {
+    float2 t = part_top[0];
+    for (int i = 1; i < 8; ++i) t = make_float2(fmaxf(t.x, part_top[i].x), fmaxf(t.y, part_top[i].y));
+    return t;
   };
   if (is_v) {
     for (int r = warp; r < nrows; r += 8) {
       const uint16_t* p = v + rf_row_offset(g, s, g.n2, n, r0 + r) + lane * kPer;
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) finite_max(decode(p[c]));
+      for (int c = 0; c < kPer; ++c) finite_max(top.x, decode(p[c]));
     }
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    if (lane == 0) atomicMax(amax + 1, __float_as_uint(top));
+    top.x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top.x)));
+    if (lane == 0) part_top[warp] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) v_blk[(size_t)n * g.t_qblk + tb] = block_top().x;
     return;
   }
   const size_t row_id = (size_t)tb * g.n1 + n;
@@ -926,7 +975,7 @@ __global__ void __launch_bounds__(256)
   const size_t lrow = (g.layout == RF_LAYOUT_BNSD ? (size_t)s.batch_idx * s.L : (size_t)s.row_off) + r0;
   float sum2 = 0.f;
   for (int r = warp; r < RF_BLOCK; r += 8) {
-    float e1 = 0.f, e2 = 0.f;
+    float e1 = 0.f, e2 = 0.f, row_top = 0.f;
     if (r < nrows) {
       const size_t off = rf_row_offset(g, s, g.n1, n, r0 + r) + lane * kPer;
       uint16_t u[kPer];
@@ -945,7 +994,7 @@ __global__ void __launch_bounds__(256)
         const float x = decode(u[c]);
         e1 = fmaf(x, m1[c], e1);
         e2 = fmaf(x, m2[c], e2);
-        if constexpr (!kBf16) finite_max(x);
+        if constexpr (!kBf16) finite_max(row_top, x);
       }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) {
@@ -954,6 +1003,13 @@ __global__ void __launch_bounds__(256)
       }
     }
     sum2 += e2;
+    if constexpr (!kBf16) {
+      row_top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(row_top)));
+      top.x = fmaxf(top.x, row_top);
+      finite_max(top.y, e1);
+      finite_max(top.y, e2);
+      if (lane == 0) do_row[((size_t)n * g.t_qblk + tb) * RF_BLOCK + r] = row_top;
+    }
     if (lane == 0) {
       float* o = st + (r >> 6) * 256 + (r & 63);
       o[0] = r < nrows ? -lse[(size_t)n * rows_total + lrow + r] : -INFINITY;
@@ -963,17 +1019,14 @@ __global__ void __launch_bounds__(256)
     }
   }
   if (lane == 0) part[warp] = sum2;
-  if constexpr (!kBf16) {
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    if (lane == 0) atomicMax(amax, __float_as_uint(top));
-    if (threadIdx.x == 0 && fabsf(lambda[n]) < INFINITY) atomicMax(amax + 2, __float_as_uint(fabsf(lambda[n])));
-  }
+  if (!kBf16 && lane == 0) part_top[warp] = top;
   __syncthreads();
   if (threadIdx.x == 0) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += part[i];
     dlam[(size_t)n * g.t_qblk + tb] = sum;
+    if constexpr (!kBf16) do_blk[(size_t)n * g.t_qblk + tb] = block_top();
   }
   if (warp == 0) {
     int bad = (lane == 0 && num != num_raw) ? 1 : 0;
@@ -1005,7 +1058,7 @@ __global__ void __launch_bounds__(256) rf_diff_dlam_kernel(const float* part, in
 template <int D, bool kBf16>
 rf_status_t launch_t(const rf_plan* p, const BwdArgs& a, const void* q_r, const void* k_r, const void* v_r,
                      const void* do_r, const float* maps, const float* lse, float* stats, uint32_t* bits,
-                     float* dlam_part, uint32_t* amax, float* dlambda, cudaStream_t st) {
+                     float* dlam_part, float* dlambda, cudaStream_t st) {
   const RfGeomDev& g = p->g;
   const long long gq = (long long)g.t_qblk * g.n1, gkv = (long long)g.t_qblk * g.n2;
   if (gq + gkv > 0x7FFFFFFFll) return rf_fail(RF_ERR_INVALID_ARG, "grid too large");
@@ -1026,14 +1079,14 @@ rf_status_t launch_t(const rf_plan* p, const BwdArgs& a, const void* q_r, const 
   constexpr auto kkv = rf_diff_dkv_kernel<D, kBf16>;
   if ((s = rf_prepare_kernel<kq>(sq, "cudaFuncSetAttribute(rf_diff_dq_kernel)")) != RF_OK) return s;
   if ((s = rf_prepare_kernel<kkv>(skv, "cudaFuncSetAttribute(rf_diff_dkv_kernel)")) != RF_OK) return s;
-  // one memset: the bit rows, dlambda's parts and amax lie together
-  if (cudaMemsetAsync(bits, 0, (size_t)((char*)amax - (char*)bits) + 256, st) != cudaSuccess)
+  if (cudaMemsetAsync(bits, 0, (size_t)gq * a.words * 4, st) != cudaSuccess)
     return rf_check_launch("cudaMemsetAsync(rf_diff backward)");
   const unsigned prep = (unsigned)(gq + (kBf16 ? 0 : gkv));
   if ((s = rf_launch_dependent(rf_diff_prep_bwd_kernel<D, kBf16>, dim3(prep), 256, st, "rf_diff_prep_bwd_kernel", g,
-                               a.sel_idx, a.sel_num, a.lambda, static_cast<const uint16_t*>(do_r),
+                               a.sel_idx, a.sel_num, static_cast<const uint16_t*>(do_r),
                                static_cast<const uint16_t*>(v_r), maps, lse, (long long)p->rows_total, a.words, stats, bits,
-                               dlam_part, amax, a.status)) != RF_OK)
+                               dlam_part, const_cast<float*>(a.do_row), const_cast<float2*>(a.do_blk),
+                               const_cast<float*>(a.v_blk), a.status)) != RF_OK)
     return s;
   if ((s = rf_launch_dependent(rf_diff_dlam_kernel, dim3((unsigned)g.n1), 256, st, "rf_diff_dlam_kernel",
                                (const float*)dlam_part, g.t_qblk, dlambda)) != RF_OK)
@@ -1057,7 +1110,6 @@ rf_status_t rf_launch_diff_bwd(const rf_plan* p, const void* q_r, const void* k_
   float* stats = reinterpret_cast<float*>(w + lay.stats);
   uint32_t* bits = reinterpret_cast<uint32_t*>(w + lay.bits);
   float* part = reinterpret_cast<float*>(w + lay.dlam);
-  uint32_t* amax = reinterpret_cast<uint32_t*>(w + lay.amax);
   BwdArgs a;
   a.g = p->g;
   a.order = rf_order(p->g);
@@ -1066,7 +1118,9 @@ rf_status_t rf_launch_diff_bwd(const rf_plan* p, const void* q_r, const void* k_
   a.lambda = lambda;
   a.stats = stats;
   a.bits = bits;
-  a.amax = amax;
+  a.do_row = reinterpret_cast<const float*>(w + lay.do_row);
+  a.do_blk = reinterpret_cast<const float2*>(w + lay.do_blk);
+  a.v_blk = reinterpret_cast<const float*>(w + lay.v_blk);
   a.words = lay.words;
   a.dq = static_cast<uint16_t*>(dq_r);
   a.dk = static_cast<uint16_t*>(dk_r);
@@ -1076,8 +1130,8 @@ rf_status_t rf_launch_diff_bwd(const rf_plan* p, const void* q_r, const void* k_
   a.sl2 = scale * kLog2e;
   const bool bf = p->dtype == RF_BF16;
   if (p->g.d == 128)
-    return bf ? launch_t<128, true>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, amax, dlambda, st)
-              : launch_t<128, false>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, amax, dlambda, st);
-  return bf ? launch_t<64, true>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, amax, dlambda, st)
-            : launch_t<64, false>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, amax, dlambda, st);
+    return bf ? launch_t<128, true>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, dlambda, st)
+              : launch_t<128, false>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, dlambda, st);
+  return bf ? launch_t<64, true>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, dlambda, st)
+            : launch_t<64, false>(p, a, q_r, k_r, v_r, do_r, maps, lse, stats, bits, part, dlambda, st);
 }

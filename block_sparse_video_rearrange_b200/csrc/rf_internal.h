@@ -77,10 +77,12 @@ struct RfDiffLayout {
   int64_t v16;        // f16 copies of V' by block, [n2][t_qblk][128][d], rows past a block's end zero
   int64_t v_exp;      // int32 [n2][t_qblk]: block t of V' is v16 * 2^v_exp
   int64_t end_serve;  // what rf_diff_attn needs ends here
-  int64_t stats;      // float4 {lse_1, lse_2, delta_1, delta_2} per row, [n1][t_qblk][128]
+  int64_t stats;      // fp32 [n1][t_qblk][2][4][64]: per 64 rows -lse_1, -lse_2, delta_1, delta_2
   int64_t bits;       // query blocks that list a key block: uint32 [n1][t_qblk][words]
   int64_t dlam;       // per-block sums of dO . O_2, fp32 [n1][t_qblk]
-  int64_t amax;       // uint32 {largest |dO|, largest |V|} as fp32 bits (fp16 plans)
+  int64_t do_row;     // largest finite |dO| of a row, fp32 [n1][t_qblk][128] (this and the next two: fp16 plans)
+  int64_t do_blk;     // {largest finite |dO|, |delta_1| and |delta_2|} of a block, float2 [n1][t_qblk]
+  int64_t v_blk;      // largest finite |V| of a block, fp32 [n2][t_qblk]
   int64_t end;        // what rf_diff_attn_backward needs ends here
   int words;          // 32-bit words of one bit row: ceil(longest sequence's blocks / 32)
 };

@@ -474,6 +474,9 @@ RF_API rf_status_t rf_diff_attn(const rf_plan_t* plan, const void* q_r, const vo
  *               rearranged order; rf_rearrange_rows puts them back), summed over
  *               the query heads that share a key/value head; rows that nothing
  *               lists get zeros.  dlambda: fp32 [n1].
+ * A = P_1 - lambda P_2 and its gradient are rounded once to the tensors' type; fp16
+ * carries powers of two through that rounding, per query row for dq_r and per key
+ * block for dk_r and dv_r, taken from what that gradient adds up and nothing else.
  * Deterministic: no atomic additions, every sum in a fixed order. */
 RF_API rf_status_t rf_diff_attn_backward(const rf_plan_t* plan, const void* q_r, const void* k_r,
                                          const void* v_r, const int32_t* select_idx,
