@@ -65,10 +65,18 @@ constexpr int kStagesV = 2;
 constexpr uint32_t kPCol = 128;
 constexpr uint32_t kOCol = 256;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays at or below 2^8
-// V blocks more than 2^-kMaxDown below the row's largest exponent would round
-// to zero in f16 (P <= 2^8, f16's last bit 2^-24).
-constexpr int kMaxDown = 40;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays below 2^9
+constexpr float kNoRow = -1e30f;           // a row's references before its first score
+// P of block b is 2^(s + d_b - m_o), d_b <= 0 the block's V exponent below the
+// list's largest and m_o the row's running maximum of s + d_b (in steps of one):
+// the accumulator's exponent follows what the row adds up, and P's f16 rounding is
+// relative to the row's largest product.  The row's sum has a reference m_l of its
+// own, the running maximum of s, and gets P times 2^(m_o - d_b - m_l).  Where d_b is
+// so low (kFar) that P could leave fp32's range before that, rows whose P is zero in
+// f16 all over the block (below 2^-kGone) take their exponentials about the block's
+// own maximum instead, for the sum alone.
+constexpr int kFar = -60;
+constexpr float kGone = 40.0f;
 constexpr uint32_t kBoxBytes = RF_BLOCK * 128;
 // fp16 lists of up to this many blocks take P in two f16 parts, twice the P V
 // products: there a CTA's fixed cost hides them (77 and 300 keys: 14.3 and 21.1 us
@@ -99,7 +107,8 @@ struct __align__(1024) DiffSmem {
   int first;  // this CTA's part of the list begins here
   int vexp_max;
   int fine;   // P in two f16 parts
-  float row_m[2][RF_BLOCK], row_l[2][RF_BLOCK];  // running maximum and sum of each map's row
+  float row_m[2][RF_BLOCK], row_l[2][RF_BLOCK];  // reference m_l and sum of each map's row
+  float row_o[2][RF_BLOCK];                      // reference m_o of its accumulator
   int list[RF_MAX_KV_LIST];
   int vexp[RF_MAX_KV_LIST];  // by block of the sequence
 };
@@ -124,10 +133,10 @@ __device__ __forceinline__ void softmax_bar_sync() {
 }
 
 // p = 2^(s * sl2 + neg_m) for the 32 scores c0 .. c0 + 31 of a row (the first vr
-// valid), rounded to f16 pairs in the 16 TMEM columns at p_addr; the unrounded
-// values go to the paired fp32 sums.
+// valid), rounded to f16 pairs (and masked, unless kFull) in the 16 TMEM columns at
+// p_addr; the unrounded values go to the paired fp32 sums.
 template <bool kFull>
-__device__ __forceinline__ void quarter_exp(const uint32_t* sr, int c0, int vr, float sl2, float neg_m,
+__device__ __forceinline__ void quarter_exp(const uint32_t* sr, int c0, int vr, float sl2, float neg_m, uint32_t mask,
                                             uint32_t p_addr, uint64_t* acc) {
   const uint64_t sl2x2 = rf_f2(__float_as_uint(sl2), __float_as_uint(sl2));
   const uint64_t negm2 = rf_f2(__float_as_uint(neg_m), __float_as_uint(neg_m));
@@ -149,6 +158,7 @@ __device__ __forceinline__ void quarter_exp(const uint32_t* sr, int c0, int vr, 
     }
     acc[(c >> 1) & 3] = rf_add2(acc[(c >> 1) & 3], rf_f2(__float_as_uint(p0), __float_as_uint(p1)));
     pk[c >> 1] = rf_pack2<false>(p0, p1);
+    if (!kFull) pk[c >> 1] &= mask;
   }
   tmem_st16(p_addr, pk);
 }
@@ -182,6 +192,10 @@ __device__ __forceinline__ void quarter_exp_fine(const uint32_t* sr, int c0, int
   tmem_st16(p_addr, pk);
   tmem_st16(p_addr + 32, lo);
 }
+
+// Exponent of the power of two an accumulator is multiplied by at the end; what is
+// cut off below leaves fp32's range either way.
+__device__ __forceinline__ int out_exp(float m, int vexp_max) { return max((int)m + max(vexp_max, -252), -252); }
 
 __device__ __forceinline__ float acc_sum(const uint64_t* acc) {
   float s = 0.f;
@@ -434,16 +448,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ocol = lane_base + kOCol + (uint32_t)(w * 128);
     const float sl2 = a.sl2;
     const int vexp_max = sm.vexp_max;
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_o = kNoRow, m_l = kNoRow, l_run = 0.f;  // fp16 has no V exponents: one reference
+    int step = 0;                                   // m_o - m_l
     bool ok = true;
     for (int b = 0; b < nv; ++b) {
       if (!warp_wait(rf_smem_u32(&sm.bar_s_full[w]), b & 1, abort)) { ok = false; break; }
       tc_fence_after();
       const int vr = (list[b] == s.n_pb - 1) ? vr_last : RF_BLOCK;
-      // P enters the product as P * 2^-down, the step from this V block's
-      // exponent to the row's largest; it is taken inside the exponential and
-      // given back to the sum.
-      const int down = min(vexp_max - sm.vexp[list[b]], kMaxDown);
+      const int d = kBf16 ? sm.vexp[list[b]] - vexp_max : 0;
+      const bool plain = vr == RF_BLOCK && d >= kFar;
       uint32_t sr[128];
       tmem_ld32(lane_base, sr);
       tmem_ld32(lane_base + 32, sr + 32);
@@ -457,11 +470,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(rf_smem_u32(&sm.bar_pv_done[w]), (b - 1) & 1, abort)) { ok = false; break; }
         tc_fence_after();
       }
-      if (__any_sync(0xffffffffu, mx > m_run + kRescaleThreshold)) {
-        const float m_new = fmaxf(m_run, mx);
-        const float alpha = rf_ex2(m_run - m_new);
-        l_run *= alpha;
-        m_run = m_new;
+      const float mo = kBf16 ? mx + (float)d : mx;
+      if (__any_sync(0xffffffffu, mo > m_o + kRescaleThreshold || (kBf16 && mx > m_l + kRescaleThreshold))) {
+        const float o_new = fmaxf(m_o, floorf(mo)), l_new = kBf16 ? fmaxf(m_l, floorf(mx)) : o_new;
+        const float alpha = rf_ex2(m_o - o_new);
+        l_run *= kBf16 ? rf_ex2(m_l - l_new) : alpha;
+        m_o = o_new;
+        m_l = l_new;
+        step = kBf16 ? (int)(m_o - m_l) : 0;
         if (b > 0) {
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
@@ -475,7 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-      const float neg_m = -m_run - (float)down;
+      float neg_m = kBf16 ? (float)d - m_o : -m_o;
+      uint32_t mask = ~0u;
+      int up = step - d;
       if (fine) {
         // a half's two parts fill the map's P columns: the second half's go there
         // when the first half's products are complete
@@ -493,34 +511,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       } else {
-        if (vr == RF_BLOCK) {
-          quarter_exp<true>(sr, 0, vr, sl2, neg_m, pcol, acc);
-          quarter_exp<true>(sr, 32, vr, sl2, neg_m, pcol + 16, acc);
+        if (plain) {
+          quarter_exp<true>(sr, 0, vr, sl2, neg_m, mask, pcol, acc);
+          quarter_exp<true>(sr, 32, vr, sl2, neg_m, mask, pcol + 16, acc);
         } else {
-          quarter_exp<false>(sr, 0, vr, sl2, neg_m, pcol, acc);
-          quarter_exp<false>(sr, 32, vr, sl2, neg_m, pcol + 16, acc);
+          if (d < kFar && mx < m_o - (float)d - kGone) {
+            neg_m = -fmaxf(floorf(mx), kNoRow);
+            up = (int)(-neg_m - m_l);
+            mask = 0u;
+          }
+          quarter_exp<false>(sr, 0, vr, sl2, neg_m, mask, pcol, acc);
+          quarter_exp<false>(sr, 32, vr, sl2, neg_m, mask, pcol + 16, acc);
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(rf_smem_u32(&sm.bar_p_half[w]));
-        if (vr == RF_BLOCK) {
-          quarter_exp<true>(sr, 64, vr, sl2, neg_m, pcol + 32, acc);
-          quarter_exp<true>(sr, 96, vr, sl2, neg_m, pcol + 48, acc);
+        if (plain) {
+          quarter_exp<true>(sr, 64, vr, sl2, neg_m, mask, pcol + 32, acc);
+          quarter_exp<true>(sr, 96, vr, sl2, neg_m, mask, pcol + 48, acc);
         } else {
-          quarter_exp<false>(sr, 64, vr, sl2, neg_m, pcol + 32, acc);
-          quarter_exp<false>(sr, 96, vr, sl2, neg_m, pcol + 48, acc);
+          quarter_exp<false>(sr, 64, vr, sl2, neg_m, mask, pcol + 32, acc);
+          quarter_exp<false>(sr, 96, vr, sl2, neg_m, mask, pcol + 48, acc);
         }
       }
-      l_run += acc_sum(acc) * rf_pow2(down);
+      // what is below 2^-126 does not count in a sum of at least 2^-9
+      l_run = kBf16 ? fmaf(acc_sum(acc), rf_pow2(max(up, -126)), l_run) : l_run + acc_sum(acc);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(rf_smem_u32(&sm.bar_p_full[w]));
     }
     if (!ok) record_timeout(abort, a.status, 3);
 
-    // Epilogue: O = 2^e_max (O_1 / l_1 - lambda O_2 / l_2).
-    sm.row_m[w][r] = m_run;
+    // Epilogue: O_w = 2^(e_max + m_o - m_l) (accumulator) / l, then O_1 - lambda O_2.
+    sm.row_m[w][r] = m_l;
     sm.row_l[w][r] = l_run;
+    sm.row_o[w][r] = m_o;
     softmax_bar_sync();
     const bool have = nv > 0 && !*abort && warp_wait(rf_smem_u32(&sm.bar_final), 0, abort) && !*abort;
     const size_t lrow = bnsd ? (size_t)s.batch_idx * s.L : (size_t)s.row_off;
@@ -536,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // row's own thread, 16 bytes here and there, the two fp32 maps took 11,000
       // cycles a CTA (now 2,000).
       const float f = have ? 1.0f / l_run : 0.f;
+      const int up = out_exp(m_o - m_l, vexp_max);
       const int cols = (warp & 3) * 32 < q_rows ? D : 0;  // none of a warp without rows
 #pragma unroll 1
       for (int c0 = 0; c0 < cols; c0 += 32) {
@@ -544,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(ocol + c0, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(rf_scale_pow2(f * __uint_as_float(o[c]), vexp_max));
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(rf_scale_pow2(f * __uint_as_float(o[c]), up));
         } else {
 #pragma unroll
           for (int c = 0; c < 32; ++c) o[c] = 0u;
@@ -555,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if constexpr (kTrain) {
         if (r < q_rows)
-          a.lse[((size_t)w * g.n1 + n) * a.rows_total + lrow + q_r0 + r] = have ? m_run + log2f(l_run) : INFINITY;
+          a.lse[((size_t)w * g.n1 + n) * a.rows_total + lrow + q_r0 + r] = have ? m_l + log2f(l_run) : INFINITY;
       }
       softmax_bar_sync();
 #pragma unroll 4
@@ -582,30 +608,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (size > 1) {
       cluster_sync();
       // this CTA merges rows [rank, rank + 1) * 128 / size: first each part's factor
-      // 2^(m_k - m) / l per row and map (where the V exponents were), then the parts
+      // 2^(m_o,k - m_o) / l per row and map and the power of two of their sum (where
+      // the V exponents were), then the parts
       const int rows = RF_BLOCK / size;
-      const uint32_t buf = parts, am = rf_smem_u32(&sm.row_m[0][0]), al = rf_smem_u32(&sm.row_l[0][0]);
+      const uint32_t buf = parts, am = rf_smem_u32(&sm.row_m[0][0]), al = rf_smem_u32(&sm.row_l[0][0]),
+                     ao = rf_smem_u32(&sm.row_o[0][0]);
       float* fac = reinterpret_cast<float*>(sm.vexp);  // [size][2][rows]
+      int* ups = sm.vexp + 2 * RF_BLOCK;               // [2][rows]
       if (threadIdx.x < 2 * rows) {
         const int x = threadIdx.x / rows, lr = threadIdx.x - x * rows, row = rank * rows + lr;
-        float mk[8], lk[8], top = -INFINITY, l = 0.f;
+        float mk[8], lk[8], ok[8], top = -INFINITY, top_o = -INFINITY, l = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          mk[k] = k < size ? cluster_ld(cluster_addr(am + 4u * (x * RF_BLOCK + row), k)) : 0.f;
-          lk[k] = k < size ? cluster_ld(cluster_addr(al + 4u * (x * RF_BLOCK + row), k)) : 0.f;
+          const uint32_t at = 4u * (x * RF_BLOCK + row);
+          mk[k] = k < size ? cluster_ld(cluster_addr(am + at, k)) : 0.f;
+          lk[k] = k < size ? cluster_ld(cluster_addr(al + at, k)) : 0.f;
+          ok[k] = k < size ? cluster_ld(cluster_addr(ao + at, k)) : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (lk[k] != 0.f) top = fmaxf(top, mk[k]);  // 0: no entries in that part
+          if (lk[k] != 0.f) {  // 0: no entries in that part, or none that counts
+            top = fmaxf(top, mk[k]);
+            top_o = fmaxf(top_o, ok[k]);
+          }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          mk[k] = lk[k] != 0.f ? rf_ex2(mk[k] - top) : 0.f;
-          l = fmaf(mk[k], lk[k], l);
+          l = lk[k] != 0.f ? fmaf(rf_ex2(mk[k] - top), lk[k], l) : l;
+          ok[k] = lk[k] != 0.f ? rf_ex2(ok[k] - top_o) : 0.f;
         }
         const float inv = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (k < size) fac[(k * 2 + x) * rows + lr] = mk[k] * inv;
+          if (k < size) fac[(k * 2 + x) * rows + lr] = ok[k] * inv;
+        ups[x * rows + lr] = l == 0.f ? 0 : out_exp(top_o - top, vexp_max);
         if constexpr (kTrain) {
           if (row < q_rows)
             a.lse[((size_t)x * g.n1 + n) * a.rows_total + lrow + q_r0 + row] = l == 0.f ? INFINITY : top + log2f(l);
@@ -631,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[x][k] = rf_scale_pow2(o[x][k], max(vexp_max, -200));
+          for (int k = 0; k < 4; ++k) o[x][k] = rf_scale_pow2(o[x][k], ups[x * rows + lr]);
         const size_t off = rf_row_offset(g, s, g.n1, n, q_r0 + row) + 4 * c;
         if constexpr (kTrain) {
           *reinterpret_cast<float4*>(a.maps + off) = make_float4(o[0][0], o[0][1], o[0][2], o[0][3]);

@@ -460,7 +460,11 @@ RF_API rf_status_t rf_diff_attn_workspace_bytes(const rf_plan_t* plan, int32_t b
  *               maps fp32 [2, shape of o_r] receives P_1 V and P_2 V, lse fp32
  *               [2, n1, rows_total] the log2 of each row's sum of exponentials
  *               (+infinity for a row without entries).
- * The difference is taken in fp32 and rounded once; P is held in f16.
+ * The difference is taken in fp32 and rounded once.  P is held in f16, relative to
+ * the row's largest product of a probability and its block's largest |V| (whatever
+ * the other listed blocks hold): off by 2^-11 of itself, or 2^-25 of that product.
+ * bf16 V is read as f16 on a power of two for each block and head: exact down to
+ * 2^-29 of the block's largest value.
  * Values of K and V rows outside the listed blocks never reach O, whatever they
  * are.  Deterministic. */
 RF_API rf_status_t rf_diff_attn(const rf_plan_t* plan, const void* q_r, const void* k_r,

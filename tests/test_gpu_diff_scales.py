@@ -108,3 +108,97 @@ def test_fp16_gradients_beside_a_large_value_elsewhere(d):
         off = (getattr(b, nm + "_r")[:first].double() - want[nm][:first]).abs()
         tol = want[nm + "_tol"][:first]
         assert (off <= tol).all(), (nm, float((off / tol).max()))
+
+
+# ---- V blocks of very different size ----------------------------------------------------------
+
+def sized_layer(power, gap, heads, zero=False):
+    """Text of five blocks; every row scores its target block 2^gap above the others, and the blocks' V are 1, 2^power,
+    1, 2^-power and 1 (or 0) in size.  Rows of every block have every target."""
+    d, blocks = 128, 5
+    plan = rf.Plan([(128 * blocks, 0, 0, 0)], heads, heads, d, "BNSD", "bf16", 0.5)
+    gen = torch.Generator().manual_seed(77)
+    n = 128 * blocks
+    q, k = (0.5 * torch.randn(n, d, generator=gen) for _ in range(2))
+    code = math.sqrt(gap * 8 * math.log(2))                   # code^2 / 8 (the scale) is 2^gap in the exponential
+    own = torch.arange(n) // 128
+    target = torch.arange(n) % blocks
+    for h in (0, 64):                                         # both maps
+        q[torch.arange(n), h + target] += code
+        k[torch.arange(n), h + own] += code
+    v = torch.randn(n, d, generator=gen)
+    v[128:256] *= 2.0 ** power
+    v[384:512] *= 2.0 ** -power
+    if zero:
+        v[512:] = 0
+    do = torch.randn(n, d, generator=gen)
+    q, k, v, do = (x.to(torch.bfloat16).cuda().expand(1, heads, n, d).contiguous() for x in (q, k, v, do))
+    si, sn = plan.select_shapes()
+    idx = torch.arange(si[2], dtype=torch.int32, device="cuda").expand(si).contiguous()
+    num = torch.full(sn, blocks, dtype=torch.int32, device="cuda")
+    return plan, q, k, v, do, idx, num, torch.full((heads,), 0.7, device="cuda")
+
+
+def sized_reference(q, k, v, do, lam, scale):
+    """One dense head in 64 bits: {name: (value, bound)}.  As in diff_ref, but for P's smallest step in the forward product:
+    f16's 2^-25, counted from the row's largest product of a probability and its block's largest |V|.  The backward pass
+    makes P = 2^(s - lse) itself, in fp32, whose normal numbers end at 2^-126: a smaller P is 0 there, so P may be off by
+    that much whatever its size (a score 130 below the row's largest, times a dA of 2^55, is a dS of 2^-75 that is lost
+    beside the dS of 2^-55 of blocks as small as 2^-55)."""
+    q, k, v, do = (x.double() for x in (q, k, v, do))
+    u, step, fp32, least = 2.0 ** -8, diff_ref.P_STEP, diff_ref.FP32, 2.0 ** -126
+    h = q.shape[1] // 2
+    size = v.abs().view(-1, 128 * v.shape[1]).amax(1)
+    size = torch.where(size > 0, 2.0 ** torch.ceil(torch.log2(size.clamp_min(1e-300))), 0.0)      # per block
+    inv = torch.where(size > 0, 1 / size.clamp_min(1e-300), 0.0).repeat_interleave(128)
+    p, o, e, lse = [], [], [], []
+    for w in (0, 1):
+        s = scale * (q[:, w * h:w * h + h] @ k[:, w * h:w * h + h].T)
+        x = torch.softmax(s, 1)
+        weight = (x * size.repeat_interleave(128)).amax(1, keepdim=True)
+        p.append(x)
+        o.append(x @ v)
+        e.append((step + fp32) * (x @ v.abs()) + 2.0 ** -25 * weight * (v.abs() * inv[:, None]).sum(0))
+        lse.append(torch.logsumexp(s, 1) / math.log(2.0))
+    out, err = o[0] - lam * o[1], e[0] + abs(lam) * e[1]
+    got = {"o": (out, u * (out.abs() + err) + err)}
+    da, da_abs = do @ v.T, do.abs() @ v.abs().T
+    a = p[0] - lam * p[1]
+    a_err = u * a.abs() + (1 + u) * (fp32 * (p[0] + abs(lam) * p[1]) + least * (1 + abs(lam)))
+    dv = a.T @ do
+    got["dv"] = (dv, a_err.T @ do.abs())
+    dq, dq_e, dk, dk_e = (torch.zeros_like(q) for _ in range(4))
+    for w, c in ((0, 1.0), (1, -lam)):
+        delta = (p[w] * da).sum(1, keepdim=True)
+        ds = c * p[w] * (da - delta)
+        d_err = (do.abs() * e[w]).sum(1, keepdim=True) + fp32 * (p[w] * da_abs).sum(1, keepdim=True)
+        ds_e = u * ds.abs() + (1 + u) * abs(c) * (p[w] * (d_err + fp32 * (da_abs + delta.abs())) + least * (da_abs + delta.abs()))
+        cols = slice(w * h, w * h + h)
+        dq[:, cols], dq_e[:, cols] = scale * (ds @ k[:, cols]), scale * (ds_e @ k[:, cols].abs())
+        dk[:, cols], dk_e[:, cols] = scale * (ds.T @ q[:, cols]), scale * (ds_e.T @ q[:, cols].abs())
+    got["dq"], got["dk"] = (dq, dq_e), (dk, dk_e)
+    for nm in ("dq", "dk", "dv"):
+        x, t = got[nm]
+        got[nm] = (x, t + u * (x.abs() + t))
+    return got, lse
+
+
+# heads = 1: the list over a cluster of CTAs; heads = 160: one CTA a list
+@pytest.mark.parametrize("heads", [1, 160])
+@pytest.mark.parametrize("power,gap,zero", [(18, 40, False), (24, 40, False), (30, 40, False), (30, 30, False), (30, 12, True),
+                                            (40, 90, True), (55, 130, False), (20, 150, True)])
+def test_rows_that_attend_to_small_v_beside_large(power, gap, zero, heads):
+    plan, q, k, v, do, idx, num, lam = sized_layer(power, gap, heads, zero)
+    b = grads(plan, q, k, v, do, idx, num, lam)
+    want, lse = sized_reference(q[0, 0], k[0, 0], v[0, 0], do[0, 0], 0.7, 1 / 8)
+    for nm, got in (("o", b.o_r), ("dv", b.dv_r), ("dk", b.dk_r), ("dq", b.dq_r)):
+        assert torch.equal(got, got[:, :1].expand_as(got)), nm
+        value, tol = want[nm]
+        off = (got[0, 0].double() - value).abs()
+        assert (off <= tol + 2.0 ** -120).all(), (nm, float((off / tol.clamp_min(1e-300)).max()))
+    for w in (0, 1):
+        assert ((b.lse[w, 0].double() - lse[w]).abs() <= 256 * 2.0 ** -22 + diff_ref.FP32).all()
+    serve = rf.DiffBuffers(plan)
+    serve.lam.copy_(lam)
+    rf.diff_attn(plan, q, k, v, idx, num, serve.lam, 1 / 8, serve.o_r, serve.ws)
+    assert torch.equal(serve.o_r, b.o_r)
