@@ -600,7 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // group w leaves its O_w there
-      if (!have) sm.row_l[w][r] = 0.f;
+      if (!have) {
+        sm.row_m[w][r] = -INFINITY;
+        sm.row_l[w][r] = 0.f;
+      }
       const uint32_t buf = parts + (uint32_t)w * (RF_BLOCK * D * 4);
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) store_part<D, 32>(buf, ocol + c0, have, r, c0);
@@ -618,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (threadIdx.x < 2 * rows) {
         const int x = threadIdx.x / rows, lr = threadIdx.x - x * rows, row = rank * rows + lr;
         float mk[8], lk[8], ok[8], top = -INFINITY, top_o = -INFINITY, l = 0.f;
+        bool any = false;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const uint32_t at = 4u * (x * RF_BLOCK + row);
@@ -626,24 +630,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok[k] = k < size ? cluster_ld(cluster_addr(ao + at, k)) : 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 8; ++k) {
+          any |= k < size && mk[k] != -INFINITY;
           if (lk[k] != 0.f) {  // 0: no entries in that part, or none that counts
             top = fmaxf(top, mk[k]);
             top_o = fmaxf(top_o, ok[k]);
           }
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           l = lk[k] != 0.f ? fmaf(rf_ex2(mk[k] - top), lk[k], l) : l;
           ok[k] = lk[k] != 0.f ? rf_ex2(ok[k] - top_o) : 0.f;
         }
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        const float inv = !any ? 0.f : 1.0f / l;  // entries whose scores are all -infinity give NaN
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < size) fac[(k * 2 + x) * rows + lr] = ok[k] * inv;
         ups[x * rows + lr] = l == 0.f ? 0 : out_exp(top_o - top, vexp_max);
         if constexpr (kTrain) {
           if (row < q_rows)
-            a.lse[((size_t)x * g.n1 + n) * a.rows_total + lrow + q_r0 + row] = l == 0.f ? INFINITY : top + log2f(l);
+            a.lse[((size_t)x * g.n1 + n) * a.rows_total + lrow + q_r0 + row] = !any ? INFINITY : top + log2f(l);
         }
       }
       softmax_bar_sync();

@@ -454,7 +454,9 @@ RF_API rf_status_t rf_diff_attn_workspace_bytes(const rf_plan_t* plan, int32_t b
  *               16-byte aligned, contiguous, in rearranged order; the entries of a
  *               selectIdx row are ascending: -1 is an unused slot, and an entry out
  *               of range, or not larger than one before it, is skipped and counted
- *               in the status words.  A row without entries gives O = 0.
+ *               in the status words.  A row without entries gives O = 0;
+ *               keys that score -infinity count for nothing, and a row whose keys
+ *               all do is NaN.
  * lambda      : fp32 [n1].
  * maps, lse   : both NULL (serving), or both given for the backward pass:
  *               maps fp32 [2, shape of o_r] receives P_1 V and P_2 V, lse fp32

@@ -202,3 +202,42 @@ def test_rows_that_attend_to_small_v_beside_large(power, gap, zero, heads):
     serve.lam.copy_(lam)
     rf.diff_attn(plan, q, k, v, idx, num, serve.lam, 1 / 8, serve.o_r, serve.ws)
     assert torch.equal(serve.o_r, b.o_r)
+
+
+# ---- scores of -infinity ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,blocks", [(1, 5), (1, 12), (160, 5)])
+def test_keys_whose_scores_are_minus_infinity_count_for_nothing(heads, blocks, dtype):
+    """A block of such keys listed first, alone, or behind the others; a row without any other key is NaN, as softmax is."""
+    d, n = 128, 128 * blocks
+    plan = rf.Plan([(n, 0, 0, 0)], heads, heads, d, "BNSD", dtype, 0.5)
+    gen = torch.Generator().manual_seed(8)
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    q, k, v = (torch.randn(n, d, generator=gen) for _ in range(3))
+    for c in (0, 64):                                          # both maps
+        q[:, c] = q[:, c].abs() + 0.1
+        k[:128, c] = k[-128:, c] = -float("inf")
+    q, k, v = (x.to(dt).cuda().expand(1, heads, n, d).contiguous() for x in (q, k, v))
+    lam = torch.full((heads,), 0.7, device="cuda")
+    si, sn = plan.select_shapes()
+    idx = torch.arange(blocks, dtype=torch.int32, device="cuda").expand(si).contiguous()
+    num = torch.full(sn, blocks, dtype=torch.int32, device="cuda")
+    idx[1, :, 1:], num[1] = -1, 1                              # block 1 lists the first one alone
+    idx[2, :, 0], idx[2, :, 1:], num[2] = blocks - 1, -1, 1    # block 2 the last one
+    num[3] = 0                                                 # block 3 nothing
+    b = rf.DiffBuffers(plan, train=True)
+    rf.diff_attn(plan, q, k, v, idx, num, lam, 1 / 8, b.o_r, b.ws, maps=b.maps, lse=b.lse)
+    rf.raise_on_device_fault(plan, b.ws, "test")
+    assert torch.equal(b.o_r[:, :1].expand_as(b.o_r).isnan(), b.o_r.isnan())
+    assert b.o_r[:, :, 128:384].isnan().all() and (b.o_r[:, :, 384:512] == 0).all()
+    assert torch.isposinf(b.lse[:, :, 384:512]).all() and not torch.isposinf(b.lse[:, :, 128:384]).any()
+    one = rf.Plan([(n, 0, 0, 0)], 1, 1, d, "BNSD", dtype, 0.5)
+    keep = idx[:, :1].clone()
+    keep[(keep == 0) | (keep == blocks - 1)] = -1              # the same without those keys
+    keep[1:4] = -1
+    want = diff_ref.reference(one, q[:, :1], k[:, :1].nan_to_num(neginf=0.0), v[:, :1], keep, num[:, :1], lam[:1], 1 / 8)
+    rows = torch.ones(n, dtype=torch.bool, device="cuda")
+    rows[128:512] = False
+    off = (b.o_r[0].double() - want["o"][0]).abs()
+    assert (off <= want["o_tol"][0])[:, rows].all(), float((off / want["o_tol"][0].clamp_min(1e-300))[:, rows].max())
