@@ -377,6 +377,9 @@ __device__ __forceinline__ long long chan_off(long long c, int width, long long 
   return g * sg + ((int)c - g * width);
 }
 
+// max(v, 0) that keeps a NaN: a group with an infinity has no variance.
+__device__ __forceinline__ float not_below_0(float v) { return v < 0.f ? 0.f : v; }
+
 // Per-channel partial sums of one slice of rows.  Forward: {sum(x - x0) as a
 // mean, sum of squared deviations}; backward: {sum g, sum g xh}.  A thread owns
 // VEC channels; the block's row lanes are merged in order.
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(kThreads) rf_norm_partial_kernel(const __grid_
       const float in = 1.0f / n;
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        p1[k] = fmaxf(p1[k] - p0[k] * p0[k] * in, 0.f);
+        p1[k] = not_below_0(p1[k] - p0[k] * p0[k] * in);
         p0[k] = x0[k] + p0[k] * in;
       }
     }
@@ -527,7 +530,7 @@ __global__ void __launch_bounds__(kReduceThreads) rf_norm_stats_kernel(const __g
   if (threadIdx.x == 0) {
     float* o = kBwd ? a.ws + (long long)a.batch * a.slices * 2 * ch : a.stats;
     o[2 * blockIdx.x] = kBwd ? s : ref + s;
-    o[2 * blockIdx.x + 1] = kBwd ? q : rsqrtf(fmaxf(q - s * s, 0.f) + a.eps);
+    o[2 * blockIdx.x + 1] = kBwd ? q : rsqrtf(not_below_0(q - s * s) + a.eps);
   }
 }
 
