@@ -627,6 +627,8 @@ rf_status_t check_desc(const rf_norm_desc_t* d) {
     return rf_fail(RF_ERR_UNSUPPORTED, "groups of more than 1024 channels per row are not built");
   if (d->batch > 65535 && d->span == RF_NORM_SAMPLE)
     return rf_fail(RF_ERR_UNSUPPORTED, "more than 65535 samples");
+  if (d->span == RF_NORM_SAMPLE && d->batch * d->groups > 0x7FFFFFFFll)  // one CTA each adds up their statistics
+    return rf_fail(RF_ERR_UNSUPPORTED, "too many groups over all samples");
   if (d->groups > 65535) return rf_fail(RF_ERR_UNSUPPORTED, "more than 65535 groups");
   if ((int64_t)d->groups * d->width > (1 << 30)) return rf_fail(RF_ERR_UNSUPPORTED, "too many channels");
   if (d->rows > (1ll << 30) || d->batch > (1ll << 30) || d->batch * d->rows > (1ll << 30)) return rf_fail(RF_ERR_UNSUPPORTED, "too many rows");

@@ -505,7 +505,9 @@ RF_API rf_status_t rf_rearrange_rows(const rf_plan_t* plan, int32_t heads, const
  *     mu, var : over a group's channels of one row (RF_NORM_ROW), or of all rows
  *               of a batch element (RF_NORM_SAMPLE)
  *     y = act(gamma * (x - mu) / sqrt(var + eps) + beta)
- * gamma, beta: [groups, width] of param_dtype. */
+ * gamma, beta: [groups, width] of param_dtype.
+ * Sizes beyond these give RF_ERR_UNSUPPORTED: batch * rows and groups * width 2^30,
+ * groups 65,535, and per sample batch 65,535 and batch * groups 2^31 - 1. */
 typedef enum { RF_NORM_ROW = 0, RF_NORM_SAMPLE = 1 } rf_norm_span_t;
 typedef enum { RF_ACT_NONE = 0, RF_ACT_SILU = 1 } rf_act_t;
 typedef struct {
