@@ -150,7 +150,11 @@ __device__ __forceinline__ void load_stats(const float* st, long long first_grou
   }
 }
 
-// 1 / (1 + e^-z) from the ex2 and reciprocal units (2^-21 relative together).
+// 1 / (1 + e^-z) from the ex2 and reciprocal units: off by 2^-21 + |z| 2^-23.7 of
+// itself at most (the second part from the fp32 product before ex2), for tensors of
+// every type.  z was rounded to fp32 before, which changes e^-z by |z| 2^-24 of
+// itself: expf and a division in their place (fp32 rows of 20 x 128, 16,640 of them:
+// 70 -> 96 us forward, 119 -> 144 us backward) would not undo that.
 __device__ __forceinline__ float sigmoid(float z) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + rf_ex2(-1.4426950408889634f * z)));
