@@ -79,10 +79,12 @@ constexpr int kFar = -60;
 constexpr float kGone = 40.0f;
 constexpr uint32_t kBoxBytes = RF_BLOCK * 128;
 // fp16 lists of up to this many blocks take P in two f16 parts, twice the P V
-// products: there a CTA's fixed cost hides them (77 and 300 keys: 14.3 and 21.1 us
-// either way), while on a long list they set the time (2.48 against 4.15 ms, 5
-// heads of the Wan-shaped grid), for fp16 results at their own rounding, 2e-4,
-// instead of 7e-4 where the maps are near-uniform.
+// products, for fp16 results at their own rounding, 2e-4, instead of 7e-4 where the
+// maps are near-uniform: a rounding of P that a short list does not average away.
+// It costs (us a call, D = 128, two parts against one): 8 heads of 77, 300 and 1,024
+// keys 13.4 / 12.0, 20.2 / 15.9 and 28.8 / 21.9; 160 heads, which fill the GPU, 23.8 /
+// 21.2, 70 / 55 and 314 / 206.  On a long list it would cost more (2.48 against
+// 4.15 ms, 5 heads of the Wan-shaped grid).
 constexpr int kFineBlocks = 8;
 
 template <int D>

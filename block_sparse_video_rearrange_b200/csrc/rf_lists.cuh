@@ -77,12 +77,21 @@ __device__ __forceinline__ void store_part(uint32_t buf, uint32_t taddr, bool ha
   for (int c = 0; c < N / 4; ++c) sts128(buf + part_off<D>(r, col / 4 + c), o + 4 * c);
 }
 
-// How many CTAs share a list: the size whose estimated finish is earliest.  A CTA
-// costs about kFixed blocks' time beside its list (start, first loads, epilogue);
-// a merge two more.  The launch ends no earlier than its longest CTA and no
-// earlier than the work spread over 148 SMs.  Measured (forward, us, sizes 1 / 2 /
-// 4): 74 items of up to 37 blocks at d = 64: 67 / 41 / 45; 148 such items at
-// d = 128: 76 / 68 / 95; 656 items of up to 82 blocks: 259 / 292 / 436.
+// How many CTAs share a list: the size whose estimated finish is earliest.  The
+// launch ends no earlier than its longest CTA and no earlier than the work spread
+// over 148 SMs; a CTA counts kFixed blocks beside its list, a merge kMerge more.
+// kFixed is a fit, not a measured time: a CTA's start, first loads and epilogue take
+// that of about 3.5 blocks (11,000 cycles), and the rest stands for what splitting
+// costs otherwise.  Measured with training outputs (us, sizes 1 / 2 / 4 / 8; the
+// backward kernels as the time of the whole backward call, one kernel's size varied;
+// * the rule's choice, the best in every row):
+//                                  forward            dK/dV                   dQ
+//   74 items, 37 blocks, d 64      69 43* 47 75       122 87* 89 118          101 87* 98 114
+//   148 items, 37 blocks, d 128    72 70* 99 171      151 134* 169 245        143 134* 156 215
+//   296 items, 37 blocks, d 128    92* 119 183 340    204* 230 297 451        205* 224 272 392
+//   656 items, 82 blocks, d 128    294* 368 528 892   697* 774 910 1,279      727* 775 869 1,140
+//   4/1 heads, 37 blocks, d 128    79 73* 101 172     389 232 153 144*        151 145* 172 229
+//   8/2 heads, 82 blocks, d 64     277* 323 460 762   905 594* 654 758        594* 638 753 982
 inline int rf_split(const RfGeomDev& g, int heads, int group) {
   constexpr double kFixed = 7.0, kMerge = 2.0, kSms = 148.0;
   double dense = 0, sparse = 0, dense_len = 0, sparse_len = 0, longest = 0;

@@ -16,9 +16,12 @@
 // Bound: HBM.  A row's group is held in registers, so RF_NORM_ROW moves each
 // element once; RF_NORM_SAMPLE reads x twice (the second time from L2 where it
 // fits).  Measured (bf16): rows of 20 x 128, 33,272 of them: 71 us, 4.8 TB/s;
-// 16,640 of them with SiLU, forward and backward: 46 and 83 us (the instructions of
-// the activation's derivative, not the memory, set the latter); samples of 16,128
-// x 320, two of them, with SiLU: 22 us in three dependent launches.
+// 16,640 of them with SiLU, forward and backward: 46 and 82 us.  The backward pass is
+// held by its instructions (issue slots 66 % busy, 179 warp instructions for each row
+// of a group, against 32 % of the DRAM rate and 26 % of the ex2 and reciprocal unit):
+// the sums over lanes, conversions and addresses as much as the activation's
+// derivative.  Samples of 16,128 x 320, two of them, with SiLU: 22 us in three
+// dependent launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -10,8 +10,10 @@ per query head n over the selected blocks, Q_1, Q_2 (K_1, K_2) being the two
 halves of a head's columns, with lambda made of learned vectors:
 lambda_n = exp(a_n . b_n) - exp(c_n . d_n) + lambda_init.  Both calls here are
 differentiable: q, k, v, the vectors, gamma and beta receive gradients (the
-ranking has none, as any top-k).  Everything runs in librf's kernels; torch
-provides memory, streams and the autograd graph.
+ranking has none, as any top-k).  The operators run in librf's kernels; torch
+provides memory, streams, the autograd graph and copies: of inputs that are not
+contiguous, and of a per-sequence norm's parts of a packed batch, which is one
+call for each sequence.
 """
 from __future__ import annotations
 

@@ -523,7 +523,8 @@ typedef struct {
 /* Workspace of both calls (host only). */
 RF_API rf_status_t rf_group_norm_workspace_bytes(const rf_norm_desc_t* desc, int64_t* out);
 /* stats: RF_NORM_SAMPLE: fp32 [batch, groups, 2] (8-byte aligned), receives {mu, 1 / sqrt(var +
- * eps)}, which the backward pass reads; RF_NORM_ROW: may be NULL (and so may ws).
+ * eps)}, which the backward pass reads; RF_NORM_ROW: may be NULL (and so may the
+ * forward pass's ws; the backward pass always needs one).
  * Outputs must not overlap inputs, nor (by zero or small strides) themselves. */
 RF_API rf_status_t rf_group_norm(const rf_norm_desc_t* desc, const void* x, const void* gamma,
                                  const void* beta, void* y, float* stats, void* ws,
