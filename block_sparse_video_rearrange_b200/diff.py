@@ -196,6 +196,8 @@ def group_norm(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, num_gro
         x = x.unflatten(2, (num_groups, shape[2] // num_groups))
     elif x.dim() != 4:
         raise ValueError(f"x: expected [batch, rows, channels] or [batch, rows, groups, width], got {tuple(shape)}")
+    elif num_groups is not None and num_groups != shape[2]:
+        raise ValueError(f"num_groups is {num_groups}, but x has {shape[2]} groups")
     if not x.is_cuda:
         raise ValueError("group_norm takes CUDA tensors")
     if x.stride(3) != 1 or _overlaps(x):
