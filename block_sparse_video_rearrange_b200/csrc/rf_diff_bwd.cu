@@ -28,8 +28,8 @@
 //
 // A and dS are rounded once, to the inputs' type, for the tensor cores.  fp16
 // has no room for their range, so there A and dS carry powers of two (exact to
-// undo), one for each accumulation, so that no row's gradient is scaled by what
-// it does not add up.  dQ: one per query row, from its own |dO| and the largest
+// undo), one for each accumulation, so that a large value that a gradient does not
+// add up costs it no digits.  dQ: one per query row, from its own |dO| and the largest
 // |V| of the blocks it lists.  dK, dV: one per key block, from its own |V| and
 // the |dO|, |delta| and |lambda| of the (head, query block) pairs that list it.
 // The bound on |dS| lands at 2^15; values down to 2^-29 of it stay normal.
