@@ -22,17 +22,25 @@ def test_group_norm_on_a_side_stream_keeps_its_temporaries(span, raw):
     got = [torch.empty_like(t) for t in want]
     sizes = [rf.group_norm_workspace(x, span).numel(), 2 * 3 * 2]
     side = torch.cuda.Stream()
-    torch.full((1,), 2 ** 30 + 12345, dtype=torch.int32, device="cuda")     # its kernel is loaded before the race
+
+    def junk():
+        return [torch.full((n,), 2 ** 30 + 12345, dtype=torch.int32, device="cuda") for n in sizes * 20]
+    junk()                                                # the memory is in the pool, the kernel loaded
     torch.cuda.synchronize()
     for call in (lambda s: rf.group_norm(x, gamma, beta, got[0], span=span, act="silu", stream=s),
                  lambda s: rf.group_norm_backward(x, gamma, beta, dy, stats, *got[1:], span=span, act="silu", stream=s)):
-        with torch.cuda.stream(side):
-            torch.cuda._sleep(100_000_000)            # some 50 ms before the kernels can start
-        call(side.cuda_stream if raw else side)
-        junk = [torch.full((n,), 2 ** 30 + 12345, dtype=torch.int32, device="cuda") for n in sizes * 20]
-        torch.cuda.current_stream().synchronize()     # written while the side stream still waits
-        assert not side.query()
-        torch.cuda.synchronize()
-        del junk
+        waited = False
+        for _ in range(3):                                # a busy host may be slower than the sleep
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(400_000_000)            # some 200 ms before the kernels can start
+            call(side.cuda_stream if raw else side)
+            taken = junk()
+            torch.cuda.current_stream().synchronize()     # written while the side stream still waits
+            waited = waited or not side.query()
+            torch.cuda.synchronize()
+            del taken
+            if waited:
+                break
+        assert waited
     for a, b in zip(got, want):
         assert torch.equal(a, b)
